@@ -5,7 +5,10 @@ include/svdq.h); this package is its thin Python binding. Importing it
 without a built library raises ImportError.
 """
 from . import _lib  # noqa: F401  (fails loudly when libsvdq.so is missing)
-from .api import (Conv2d, Linear, Prepared, channel_absmax, clock_mark, clock_probe,  # noqa: F401
+from .api import (Conv2d, Linear, Prepared, attention, attention_workspace_bytes,
+                  document_key_ranges, fp8_padded, gemm_fp8, gemm_fp8_workspace_bytes, linear_fp8,
+                  linear_fp8_workspace_bytes, prepare_weights_fp8, quantize_act_fp8,
+                  rmsnorm_quantize_fp8, channel_absmax, clock_mark, clock_probe,  # noqa: F401
                   clock_rates, concat_lora, int4_act_tiled_bytes, int4_act_scales_tiled_bytes, int4_d_tiled_bytes,
                   int4_w_codes_tiled_bytes, int4_w_scales_tiled_bytes, linear_tiled,
                   linear_tiled_workspace_bytes, pack_w4a4_tiles, quantize_act_lowrank_down_tiled,
@@ -21,7 +24,10 @@ from .api import (Conv2d, Linear, Prepared, channel_absmax, clock_mark, clock_pr
                   quantize_act_lowrank_down_mx, smoothing_factors, w4a4_gemm_lowrank_up,
                   w4a16_gemm, w4a16_tile_activation, w4a16_x_tiled_bytes, linear_w4a16)
 
-__all__ = ["Conv2d", "Linear", "Prepared", "channel_absmax", "clock_mark", "clock_probe",
+__all__ = ["Conv2d", "Linear", "Prepared", "attention", "attention_workspace_bytes",
+           "document_key_ranges", "fp8_padded", "gemm_fp8", "gemm_fp8_workspace_bytes",
+           "linear_fp8", "linear_fp8_workspace_bytes", "prepare_weights_fp8",
+           "quantize_act_fp8", "rmsnorm_quantize_fp8", "channel_absmax", "clock_mark", "clock_probe",
            "clock_rates", "concat_lora", "int4_act_tiled_bytes", "int4_act_scales_tiled_bytes", "int4_d_tiled_bytes",
            "int4_w_codes_tiled_bytes", "int4_w_scales_tiled_bytes", "linear_tiled",
            "linear_tiled_workspace_bytes", "pack_w4a4_tiles", "quantize_act_lowrank_down_tiled",

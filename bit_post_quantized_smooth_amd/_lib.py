@@ -31,9 +31,10 @@ lib = C.CDLL(LIB_PATH)
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_DTYPE, ERR_RANK, ERR_WORKSPACE, ERR_HIP, \
     ERR_NO_DEVICE, ERR_INTERNAL, ERR_GROUP, ERR_ACT = range(12)
 ACT_NONE, ACT_GELU_TANH = 0, 1
-F16, F32 = 1, 2
+F16, F32, BF16 = 1, 2, 3
 GROUP = 64
 MX_BLOCK = 32
+FP8_BLOCK = 128
 MAX_RANK = 256
 NOALLOC_MAX_BYTES = 64 << 20
 
@@ -41,6 +42,7 @@ _p = C.c_void_p
 _i64 = C.c_int64
 _i32 = C.c_int32
 _int = C.c_int
+_f = C.c_float
 
 _SIGS = {
     "svdq_abi_version": (_int, []),
@@ -116,6 +118,19 @@ _SIGS = {
                               _p, _i32, _p, _p, _p, _p, _int, _i64, _p, C.c_size_t, _i32, _p]),
     "svdq_debug_group_partials": (_int, [_p, _p, _i64, _i64, _i64, _i32, _i64, _i64, _p, _p]),
     "svdq_gelu_tanh_f16": (_int, [_p, _p, _i64, _p]),
+    "svdq_prepare_weights_fp8": (_int, [_p, _i64, _i64, _p, _p]),
+    "svdq_rmsnorm_quantize_fp8": (_int, [_p, _p, _int, _i64, _i64, _i64, _i64, _p, _f, _p, _p, _p,
+                                         _i64, _p]),
+    "svdq_quantize_act_fp8": (_int, [_p, _int, _i64, _i64, _i64, _p, _p, _p]),
+    "svdq_gemm_fp8_workspace_bytes": (C.c_size_t, [_i64, _i64, _i64]),
+    "svdq_gemm_fp8": (_int, [_p, _p, _p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _i32, _p,
+                             C.c_size_t, _p]),
+    "svdq_linear_fp8_workspace_bytes": (C.c_size_t, [_i64, _i64, _i64]),
+    "svdq_linear_fp8": (_int, [_p, _int, _i64, _p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _p,
+                               C.c_size_t, _i32, _p]),
+    "svdq_attention_workspace_bytes": (C.c_size_t, [_i64, _i64, _i64, _i64, _i64, _i64]),
+    "svdq_attention": (_int, [_p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _p, _f, _f,
+                              _p, _i32, _p, _p, _i64, _p, C.c_size_t, _p]),
     "svdq_clock_rates": (_int, [_p, _p]),
     "svdq_clock_probe": (_int, [_p, _i32, _i64, _p, _p]),
     "svdq_clock_mark": (_int, [_p, _p, _p]),

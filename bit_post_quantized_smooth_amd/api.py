@@ -7,13 +7,14 @@ All checks and all arithmetic are done by the library.
 """
 from __future__ import annotations
 
+import ctypes
 import dataclasses
 from typing import Optional
 
 import numpy as np
 
 from . import _lib
-from ._lib import F16, F32, GROUP, MX_BLOCK, check, lib
+from ._lib import BF16, F16, F32, FP8_BLOCK, GROUP, MX_BLOCK, check, lib
 
 # --------------------------------------------------------------------------
 # host prep (numpy)
@@ -53,7 +54,9 @@ class Prepared:
     """Offline products for one layer, host side. L1t is R x K, L2t is N x R (fp16 bits).
     ``fmt`` "int4": w_scales are the fp16 group scales (N x K/64, as uint16 bits);
     ``fmt`` "mxfp4": w_scales are the E8M0 block exponents (N x K/32, uint8);
-    ``fmt`` "w4a16": the weight-only baseline, Q of W itself (rank 0, no smoothing)."""
+    ``fmt`` "w4a16": the weight-only baseline, Q of W itself (rank 0, no smoothing);
+    ``fmt`` "fp8": e4m3 codes (N x K rounded up to 128) and fp32 scales per 128 x 128
+    block (rank 0, no smoothing)."""
     K: int
     N: int
     rank: int
@@ -175,6 +178,40 @@ def prepare_weights_w4a16(W: np.ndarray) -> Prepared:
           "svdq_prepare_weights_w4a16")
     return Prepared(K, N, 0, np.ones(K, dtype=np.float32), np.empty((0, K), np.uint16),
                     np.empty((N, 0), np.uint16), wc, ws, None, fmt="w4a16")
+
+
+def prepare_weights_fp8(W: np.ndarray) -> Prepared:
+    """svdq_prepare_weights_fp8: W (K x N) in e4m3 with one scale per 128 x 128
+    block (fmt "fp8"; any K and N)."""
+    W = _c(W, np.float32)
+    K, N = W.shape
+    Kp = fp8_padded(K)
+    wc = np.empty((N, Kp), dtype=np.uint8)
+    ws = np.empty((-(-N // FP8_BLOCK), Kp // FP8_BLOCK), dtype=np.float32)
+    check(lib.svdq_prepare_weights_fp8(_np_ptr(W), K, N, _np_ptr(wc), _np_ptr(ws)),
+          "svdq_prepare_weights_fp8")
+    return Prepared(K, N, 0, np.ones(K, dtype=np.float32), np.empty((0, K), np.uint16),
+                    np.empty((N, 0), np.uint16), wc, ws, None, fmt="fp8")
+
+
+def fp8_padded(K: int) -> int:
+    """K rounded up to whole 128-channel blocks: the row length of e4m3 codes."""
+    return -(-K // FP8_BLOCK) * FP8_BLOCK
+
+
+def document_key_ranges(lengths, L: int | None = None) -> np.ndarray:
+    """The key ranges (int32, 1 x L x 2) of documents of the given lengths packed one
+    after the other: a row sees its own document; rows past the last one (padding up
+    to L) see nothing. For ``attention(key_ranges=...)``, on the device."""
+    ends = np.cumsum(np.asarray(lengths, dtype=np.int64))
+    used = int(ends[-1]) if len(ends) else 0
+    L = used if L is None else L
+    if np.any(np.asarray(lengths) < 0) or used > L:
+        raise ValueError(f"documents of {used} tokens in a sequence of {L}")
+    r = np.zeros((1, L, 2), dtype=np.int32)
+    for b, e in zip(np.concatenate(([0], ends[:-1])) if len(ends) else (), ends):
+        r[0, b:e] = (b, e)
+    return r
 
 
 def pack_w4a16_tiles(w_codes: np.ndarray, w_scales: np.ndarray, K: int):
@@ -869,12 +906,180 @@ def gelu_tanh_f16(x, y, stream=None):
     check(lib.svdq_gelu_tanh_f16(_tp(x), _tp(y), x.numel(), _stream(stream)), "svdq_gelu_tanh_f16")
 
 
+# --------------------------------------------------------------------------
+# the 8-bit attention block
+
+_BLOCK_X = ("float16", "bfloat16", "float32")
+_E4M3 = ("uint8", "int8", "float8_e4m3fn")
+
+
+def _dt_block(t) -> int:
+    torch = _torch()
+    return BF16 if t.dtype == torch.bfloat16 else _dt(t)
+
+
+def _ld(t) -> int:
+    """Row stride of a checked matrix (one row may have any)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _fp8_side(name, rows, Kp, codes, scales, srows):
+    _buf(name + "_codes", codes, _E4M3, nbytes=rows * Kp)
+    _buf(name + "_scales", scales, _F32, nbytes=4 * srows * (Kp // FP8_BLOCK))
+
+
+def rmsnorm_quantize_fp8(X, residual, gain, eps: float, a_codes, a_scales, residual_out=None,
+                         stream=None):
+    """svdq_rmsnorm_quantize_fp8: h = X + residual (may be None), written to
+    residual_out (may be None, or X or residual itself); the RMS norm of h times
+    gain (may be None) as e4m3 codes (M x fp8_padded(K)) and fp32 scales (M x
+    fp8_padded(K)/128)."""
+    _mat("X", X, None, None, _BLOCK_X)
+    M, K = X.shape
+    for name, t in (("residual", residual), ("residual_out", residual_out)):
+        if t is not None:
+            _mat(name, t, M, K, _BLOCK_X)
+            if t.dtype != X.dtype:
+                raise ValueError(f"{name}: dtype {t.dtype}, X has {X.dtype}")
+    if gain is not None:
+        _buf("gain", gain, _F32, nbytes=4 * K)
+    _fp8_side("a", M, fp8_padded(K), a_codes, a_scales, M)
+    _on_gpu(X, residual, residual_out, gain, a_codes, a_scales)
+    check(lib.svdq_rmsnorm_quantize_fp8(
+        _tp(X), _tp(residual), _dt_block(X), M, K, _ld(X), _ld(residual) if residual is not None
+        else 0, _tp(gain), float(eps), _tp(a_codes), _tp(a_scales), _tp(residual_out),
+        _ld(residual_out) if residual_out is not None else 0, _stream(stream)),
+        "svdq_rmsnorm_quantize_fp8")
+
+
+def quantize_act_fp8(X, a_codes, a_scales, stream=None):
+    """svdq_quantize_act_fp8: X as e4m3 codes and one fp32 scale per row and 128 channels."""
+    _mat("X", X, None, None, _BLOCK_X)
+    M, K = X.shape
+    _fp8_side("a", M, fp8_padded(K), a_codes, a_scales, M)
+    _on_gpu(X, a_codes, a_scales)
+    check(lib.svdq_quantize_act_fp8(_tp(X), _dt_block(X), M, K, _ld(X), _tp(a_codes),
+                                    _tp(a_scales), _stream(stream)), "svdq_quantize_act_fp8")
+
+
+def gemm_fp8_workspace_bytes(M: int, N: int, Kp: int) -> int:
+    return int(lib.svdq_gemm_fp8_workspace_bytes(M, N, Kp))
+
+
+def gemm_fp8(a_codes, a_scales, w_codes, w_scales, bias, Y, ws=None, stream=None,
+             activation=None):
+    """svdq_gemm_fp8: Y (M x N) from e4m3 codes a (M x Kp) and w (N x Kp) and their
+    scales (M x Kp/128 and ceil(N/128) x Kp/128). With a workspace of
+    gemm_fp8_workspace_bytes a shape of few tiles and long K is split along K."""
+    _mat("Y", Y, None, None, _BLOCK_X)
+    M, N = Y.shape
+    _mat("a_codes", a_codes, M, None, _E4M3)
+    Kp = a_codes.shape[1]
+    if Kp < FP8_BLOCK or Kp % FP8_BLOCK:
+        raise ValueError(f"a_codes: {Kp} columns, need a positive multiple of {FP8_BLOCK}")
+    _fp8_side("a", M, Kp, a_codes, a_scales, M)
+    _fp8_side("w", N, Kp, w_codes, w_scales, -(-N // FP8_BLOCK))
+    _bias(bias, N)
+    if ws is not None:
+        _buf("ws", ws, _BYTES + _HALF + _F32)
+    _on_gpu(a_codes, a_scales, w_codes, w_scales, bias, Y, ws)
+    check(lib.svdq_gemm_fp8(_tp(a_codes), _tp(a_scales), _tp(w_codes), _tp(w_scales), _tp(bias),
+                            _tp(Y), _dt_block(Y), M, N, Kp, _ld(Y), _act(activation), _tp(ws),
+                            0 if ws is None else ws.numel() * ws.element_size(),
+                            _stream(stream)), "svdq_gemm_fp8")
+
+
+def linear_fp8_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib.svdq_linear_fp8_workspace_bytes(M, K, N))
+
+
+def linear_fp8(X, w_codes, w_scales, bias, Y, ws, stream=None, activation=None):
+    """svdq_linear_fp8: the 8-bit linear layer, X (M x K) quantized into ws, then the
+    product with the e4m3 weights of prepare_weights_fp8."""
+    _mat("X", X, None, None, _BLOCK_X)
+    M, K = X.shape
+    _mat("Y", Y, M, None, _BLOCK_X)
+    N = Y.shape[1]
+    _fp8_side("w", N, fp8_padded(K), w_codes, w_scales, -(-N // FP8_BLOCK))
+    _bias(bias, N)
+    _buf("ws", ws, _BYTES + _HALF + _F32, min_bytes=linear_fp8_workspace_bytes(M, K, N))
+    _on_gpu(X, w_codes, w_scales, bias, Y, ws)
+    check(lib.svdq_linear_fp8(_tp(X), _dt_block(X), _ld(X), _tp(w_codes), _tp(w_scales),
+                              _tp(bias), _tp(Y), _dt_block(Y), _ld(Y), M, K, N, _tp(ws),
+                              ws.numel() * ws.element_size(), _act(activation),
+                              _stream(stream)), "svdq_linear_fp8")
+
+
+def attention_workspace_bytes(B: int, Lq: int, Lk: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib.svdq_attention_workspace_bytes(B, Lq, Lk, Hq, Hkv, D))
+
+
+def _heads(name, t, B, L, H, D, dtype):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected float16 or bfloat16")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, Q has {dtype}")
+    if t.dim() != 4 or any(w is not None and s != w for s, w in zip(t.shape, (B, L, H, D))):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(B, L, H, D)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: the inner stride must be 1, got {t.stride(3)}")
+    # a dimension of one (or of none) is never stepped over: its stride is free
+    return [t.stride(i) if t.shape[i] > 1 else t.shape[3] if i == 1 else 0 for i in range(3)]
+
+
+def attention(Q, K, V, Out, scale: float | None = None, softcap: float = 0.0, slopes=None,
+              causal: bool = False, prefix=None, key_ranges=None, ws=None, stream=None):
+    """svdq_attention: Out (B x Lq x Hq x D) from Q (B x Lq x Hq x D), K and V (B x Lk x
+    Hkv x D), fp16 or bf16, strided views with contiguous channels.
+
+    scale: of the scores, D**-0.5 by default; softcap > 0: scores through softcap *
+    tanh(x / softcap); slopes (fp32, Hq): minus slope * distance; causal: query i sees keys
+    up to i + Lk - Lq, and with prefix (int32, B) the first prefix[b] keys besides;
+    key_ranges (int32, B or 1 x Lq x 2): query i sees keys [begin, end) only
+    (document_key_ranges; the filled part of a cache). A row that sees no key is 0.
+    With a workspace of attention_workspace_bytes few rows over many keys are split
+    along the keys."""
+    sq_ = _heads("Q", Q, None, None, None, None, None)
+    B, Lq, Hq, D = Q.shape
+    sk = _heads("K", K, B, None, None, D, Q.dtype)
+    Lk, Hkv = K.shape[1], K.shape[2]
+    sv = _heads("V", V, B, Lk, Hkv, D, Q.dtype)
+    so = _heads("Out", Out, B, Lq, Hq, D, Q.dtype)
+    if Hkv < 1 or Hq < 1 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads over {Hkv} key heads")
+    if prefix is not None:
+        if not causal:
+            raise ValueError("prefix: needs causal=True")
+        _buf("prefix", prefix, ("int32",), nbytes=4 * B)
+    if slopes is not None:
+        _buf("slopes", slopes, _F32, nbytes=4 * Hq)
+    rb = 0
+    if key_ranges is not None:
+        _buf("key_ranges", key_ranges, ("int32",))
+        if tuple(key_ranges.shape) not in ((B, Lq, 2), (1, Lq, 2)):
+            raise ValueError(f"key_ranges: shape {tuple(key_ranges.shape)}, expected "
+                             f"({B}, {Lq}, 2) or (1, {Lq}, 2)")
+        rb = 2 * Lq if key_ranges.shape[0] > 1 else 0
+    if ws is not None:
+        _buf("ws", ws, _BYTES + _HALF + _F32)
+    _on_gpu(Q, K, V, Out, slopes, prefix, key_ranges, ws)
+    strides = (ctypes.c_int64 * 12)(*sq_, *sk, *sv, *so)
+    check(lib.svdq_attention(
+        _tp(Q), _tp(K), _tp(V), _tp(Out), _dt_block(Q), B, Lq, Lk, Hq, Hkv, D, strides,
+        D ** -0.5 if scale is None else float(scale), float(softcap), _tp(slopes),
+        1 if causal else 0, _tp(prefix), _tp(key_ranges), rb, _tp(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "svdq_attention")
+
+
 class Linear:
     """One prepared SVDQuant layer resident on a device.
 
     ``Linear(prep, bias)(X)`` runs K1 then K2 (their MXFP4 versions for a
     prep of fmt "mxfp4"; with ``tiled=True`` an INT4 prep runs the tiled path,
-    svdq_linear_tiled) on the current stream and
+    svdq_linear_tiled; a prep of fmt "fp8" runs svdq_linear_fp8) on the current stream and
     returns Y (M x N, ``out_dtype``), optionally through the fused activation
     (``"gelu_tanh"``). The workspace is kept between calls and grown when a
     larger M arrives."""
@@ -897,6 +1102,9 @@ class Linear:
             ct, st = pack_w4a16_tiles(prep.w_codes, prep.w_scales, prep.K)
             self.w_codes = torch.from_numpy(ct).to(dev)
             self.w_scales = torch.from_numpy(st.view(np.int16)).to(dev)
+        elif self.fmt == "fp8":
+            self.w_codes = torch.from_numpy(prep.w_codes).to(dev)
+            self.w_scales = torch.from_numpy(prep.w_scales).to(dev)
         elif self.fmt == "mxfp4":
             ct, et = pack_mx_tiles(prep.w_codes, prep.w_scales, prep.K)
             self.w_codes = torch.from_numpy(ct).to(dev)
@@ -914,6 +1122,8 @@ class Linear:
         torch = _torch()
         if self.fmt == "w4a16":
             need = w4a16_x_tiled_bytes(M, self.K)
+        elif self.fmt == "fp8":
+            need = linear_fp8_workspace_bytes(M, self.K, self.N)
         elif self.fmt == "mxfp4":
             need = linear_mx_workspace_bytes(M, self.K, self.R)
         elif self.tiled:
@@ -928,16 +1138,21 @@ class Linear:
 
     def __call__(self, X, Y=None, stream=None):
         torch = _torch()
-        _mat("X", X, None, self.K)
+        types = _BLOCK_X if self.fmt == "fp8" else _XY
+        _mat("X", X, None, self.K, types)
         M = X.shape[0]
         if Y is not None:
-            _mat("Y", Y, M, self.N)
+            _mat("Y", Y, M, self.N, types)
         if Y is None:
             Y = torch.empty((M, self.N), dtype=self.out_dtype or X.dtype, device=self.device)
         if self.fmt == "w4a16":
             if self.activation is not None:
                 raise ValueError("the weight-only baseline has no fused activation")
             linear_w4a16(X, self.w_codes, self.w_scales, self.bias, Y, self.workspace(M), stream)
+            return Y
+        if self.fmt == "fp8":
+            linear_fp8(X, self.w_codes, self.w_scales, self.bias, Y, self.workspace(M), stream,
+                       self.activation)
             return Y
         run = linear_mx if self.fmt == "mxfp4" else linear_tiled if self.tiled else linear
         run(X, self.inv_smooth, self.L1p, self.L2t, self.R, self.w_codes, self.w_scales,

@@ -22,10 +22,12 @@ ARCH = "gfx950"
 HIP_SOURCES = ["k1_quant_down.hip", "k2_w4a4_gemm.hip", "k2_mx_gemm.hip", "k2_w4a16_gemm.hip",
                "k2_w4a4_tiled.hip", "gelu.hip", "lowrank_pack.hip", "clock_probe.hip",
                "abi_device.hip",
-               "abi_noalloc.hip"]
+               "abi_noalloc.hip", "fp8_quant.hip", "fp8_gemm.hip", "attention.hip",
+               "abi_block.hip"]
 HOST_SOURCES = {
     # the quantizer's fp32 divide/multiply must round exactly: no contraction
     "host_prep.cpp": ["-ffp-contract=off"],
+    "host_fp8.cpp": ["-ffp-contract=off"],
     # the eigen-solver only needs fp64 accuracy; let it use FMA and AVX2
     "host_eigen.cpp": ["-mavx2", "-mfma", "-ffp-contract=fast"],
 }

@@ -1,0 +1,569 @@
+// Masked attention with grouped heads (gfx950).
+//
+//   x_ij = scale * q_i . k_j;  with a cap: x_ij = cap * tanh(x_ij / cap);
+//   with slopes: x_ij -= slope_h * |pos_i - j|,  pos_i = i + Lk - Lq;
+//   o_i = sum_j exp(x_ij) v_j / sum_j exp(x_ij) over the keys j that row i sees.
+//
+// Every mask is an interval of keys per query row, [lo_i, hi_i): the caller's
+// ranges (documents, padding, filled part of a cache), cut by the causal rule
+// j <= pos_i, which the first `prefix` keys escape. A row that sees no key
+// comes out 0, and a key that a row does not see never reaches its output,
+// whatever its K and V hold.
+//
+// One pass over the keys with the running maximum and sum of the softmax, in
+// base 2 (log2 e goes into the scale). The query heads that share a key head
+// are rows of one problem, so each K and V tile is read once for all of them:
+// row r is query r / G of head hk*G + r % G. A wave owns 32 rows and computes
+//   S^T = K Q^T   (v_mfma_f32_32x32x16, K the first operand),
+// so a lane holds scores of one row only (row lane % 32): the softmax needs one
+// exchange between the wave's halves, and the rescaling factor of a row is in
+// the lane that holds its outputs. The same registers, rounded to 16 bits, are
+// the second operand of
+//   O^T += V^T P^T;
+// the matrix core sums over the keys in any order, so V^T is read in the order
+// in which S^T leaves the keys: a transposing LDS read (ds_read_b64_tr_b16) of
+// 4 keys x 16 channels per 16 lanes. Scores, maxima, sums and outputs are fp32;
+// P is rounded to the type of V (nearest even), the precision of the result.
+//
+// K and V go from global memory straight into LDS (two stages), rows of DP
+// channels with their 16-byte units XOR-swizzled by the row; channels past D
+// and keys outside the tile read as zero. Work is split along the keys where
+// there are few rows: over the workgroup's waves (KW = 4) and over workgroups,
+// which then write fp32 outputs with their maxima and sums for a second kernel
+// that joins them in order.
+#include <hip/hip_runtime.h>
+
+#include "../../include/svdq.h"
+#include "attention.hpp"
+#include "block_common.hpp"
+#include "k2_common.hpp"
+
+namespace svdq {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+constexpr int kWaves = 4;
+
+template <class T>
+struct Half;
+template <>
+struct Half<_Float16> {
+  typedef v8h vec;
+  static __device__ __forceinline__ v16f mfma(v8h a, v8h b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  static constexpr uint32_t kExp = 0x7C007C00u;     // exponent bits of two values
+  static constexpr uint16_t kOne = 0x3C00, kExp1 = 0x7C00, kFrac = 0x03FF;
+};
+template <>
+struct Half<__bf16> {
+  typedef v8bf vec;
+  static __device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static constexpr uint32_t kExp = 0x7F807F80u;
+  static constexpr uint16_t kOne = 0x3F80, kExp1 = 0x7F80, kFrac = 0x007F;
+};
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+
+// max over the two lanes that share a row (lane and lane ^ 32); sum likewise
+__device__ __forceinline__ void half_pair(float x, float& a, float& b) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];   // scalars: a bit cast of an element takes element 0
+  a = __builtin_bit_cast(float, r0);
+  b = __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ float half_max(float x) {
+  float a, b;
+  half_pair(x, a, b);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ float half_sum(float x) {
+  float a, b;
+  half_pair(x, a, b);
+  return a + b;
+}
+
+// RW waves along the rows, 4 / RW along the keys of a tile.
+template <class T, int DP, int RW, bool CAP, bool SLOPES>
+struct Attention {
+  static constexpr int KW = kWaves / RW;
+  static constexpr int KB = KW == 1 ? 2 : 1;        // blocks of 32 keys per wave and tile
+  static constexpr int KT = 32 * KB * KW;           // keys per tile
+  static constexpr int DB = DP / 32, DS = DP / 16;  // output blocks, steps of the dot product
+  static constexpr int UNITS = DP / 8;              // 16-byte units per row
+  static constexpr int RPC = 64 / UNITS;            // rows per copy instruction
+  static constexpr int CPW = KT / RPC / kWaves;     // copy instructions per wave and operand
+  typedef typename Half<T>::vec vec;
+
+  // one object, and reads through plain vector types: with several, or
+  // through a struct, the compiler makes every read wait for every copy
+  struct alignas(16) Lds {
+    uint8_t k[2][KT][DP * 2];
+    uint8_t v[2][KT][DP * 2];
+    int bounds[kWaves][2];
+  };
+  static_assert(KW == 1 || sizeof(Lds::k) + sizeof(Lds::v) >=
+                               static_cast<size_t>(kWaves) * 32 * (DP + 2) * 4,
+                "the waves' partial outputs are joined in the tiles' memory");
+
+  const AttnArgs& g;
+  Lds& lds;
+  int lane, wave, rl, h, kw;
+  int64_t b;
+  int hk;
+  vec qf[DS];
+  v16f o[DB];
+  float m, l;                                       // row maximum (base 2), this half's sum
+  int lo, hi, pos;                                  // the row's keys, its own position
+  int w_lo, w_hi, w_lo_max, w_hi_min;               // over the wave's rows
+  float slope2;
+  uint32_t koff[CPW], voff[CPW];
+
+  __device__ __forceinline__ Attention(const AttnArgs& args, Lds& shared) : g(args), lds(shared) {}
+
+  __device__ __forceinline__ void copy(int s, int key0, int keys) {
+    const char* kb = static_cast<const char*>(g.k) + (b * g.k_b + hk * g.k_h + key0 * g.k_l) * 2;
+    const char* vb = static_cast<const char*>(g.v) + (b * g.v_b + hk * g.v_h + key0 * g.v_l) * 2;
+    const int n = keys < KT ? keys : KT;
+    const __amdgpu_buffer_rsrc_t bk =
+        make_buffer(kb, static_cast<uint32_t>(((n - 1) * g.k_l + g.D) * 2));
+    const __amdgpu_buffer_rsrc_t bv =
+        make_buffer(vb, static_cast<uint32_t>(((n - 1) * g.v_l + g.D) * 2));
+#pragma unroll
+    for (int i = 0; i < CPW; ++i)
+      buffer_to_lds16(bk, &lds.k[s][(CPW * wave + i) * RPC][0], koff[i], 0);
+#pragma unroll
+    for (int i = 0; i < CPW; ++i)
+      buffer_to_lds16(bv, &lds.v[s][(CPW * wave + i) * RPC][0], voff[i], 0);
+  }
+
+  // The V^T operand of 16 keys (from key on) and output block d: lane (d, h)
+  // gets keys 4h .. 4h+3 and 8+4h .. 8+4h+3 of channel 32 d + lane % 32.
+  __device__ __forceinline__ v8s v_frag(int s, int key, int d) {
+    const int a = lane & 15, g16 = lane >> 4;
+    const int ch = 32 * d + 16 * (g16 & 1) + 4 * (a & 3);
+    v4s part[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = key + 8 * e + 4 * (g16 >> 1) + (a >> 2);
+      const int unit = (ch >> 3) ^ (row & (UNITS - 1));
+      const uint8_t* p = &lds.v[s][row][unit * 16 + (ch & 4) * 2];
+      part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) v4s*)(p));
+    }
+    return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+
+  // Scores of one 32-key block to base-2 logits; key0 is the key of row 0 of
+  // the block.
+  template <bool MASK>
+  __device__ __forceinline__ void logits(v16f& s, int key0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int key = key0 + (i & 3) + 8 * (i >> 2) + 4 * h;
+      float x = s[i];
+      if constexpr (CAP) {
+        // cap * tanh(y) with tanh(y) = 1 - 2 / (exp(2 y) + 1)
+        const float e = __builtin_amdgcn_exp2f(x * g.cap_in);
+        x = g.cap2 - 2.0f * g.cap2 * __builtin_amdgcn_rcpf(e + 1.0f);
+      } else {
+        x = x * g.scale2;
+      }
+      if constexpr (SLOPES) x = __builtin_fmaf(-slope2, fabsf(static_cast<float>(pos - key)), x);
+      if constexpr (MASK) x = key >= lo && key < hi ? x : kNegInf;
+      s[i] = x;
+    }
+  }
+
+  // O^T += V^T P^T for 16 keys of a block whose masks hide some of them. A
+  // hidden key has P = 0, but 0 times an infinity or a NaN in V would reach
+  // the rows that do not see it: such values are taken out of the operand, and
+  // their effect (an infinity of their sign, or NaN) is added to the rows that
+  // do see them, found as matrix products of indicators.
+  __device__ __forceinline__ void pv_masked(int s, int krow, int key0, const v8s& p) {
+    v8s sees;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int key = key0 + (e & 3) + 8 * (e >> 2) + 4 * h;
+      sees[e] = key >= lo && key < hi ? static_cast<short>(Half<T>::kOne) : short{0};
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+      v8s v = v_frag(s, krow, d);
+      bool odd = false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) odd |= (v[e] & Half<T>::kExp1) == Half<T>::kExp1;
+      if (__builtin_amdgcn_ballot_w64(odd) != 0) {
+        v8s up, down;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint16_t x = static_cast<uint16_t>(v[e]);
+          const bool bad = (x & Half<T>::kExp1) == Half<T>::kExp1;
+          const bool nan = bad && (x & Half<T>::kFrac) != 0;
+          up[e] = bad && (nan || !(x & 0x8000)) ? static_cast<short>(Half<T>::kOne) : short{0};
+          down[e] = bad && (nan || (x & 0x8000)) ? static_cast<short>(Half<T>::kOne) : short{0};
+          if (bad) v[e] = 0;
+        }
+        v16f zero;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zero[i] = 0.f;
+        const v16f nu = Half<T>::mfma(__builtin_bit_cast(vec, up), __builtin_bit_cast(vec, sees), zero);
+        const v16f nd = Half<T>::mfma(__builtin_bit_cast(vec, down), __builtin_bit_cast(vec, sees), zero);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (nu[i] > 0.f) o[d][i] = o[d][i] - kNegInf;
+          if (nd[i] > 0.f) o[d][i] = o[d][i] + kNegInf;
+        }
+      }
+      o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v), __builtin_bit_cast(vec, p), o[d]);
+    }
+  }
+
+  // One tile, whose row 0 is key0, from stage s.
+  template <bool MASK>
+  __device__ __forceinline__ void tile(int s, int key0) {
+    v16f x[KB];
+    float top = kNegInf;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const int krow = 32 * (KB * kw + kb);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[kb][i] = 0.f;
+      const int row = krow + rl;
+#pragma unroll
+      for (int t = 0; t < DS; ++t) {
+        const int unit = (2 * t + h) ^ (row & (UNITS - 1));
+        const v4i kf = *reinterpret_cast<const v4i*>(&lds.k[s][row][unit * 16]);
+        x[kb] = Half<T>::mfma(__builtin_bit_cast(vec, kf), qf[t], x[kb]);
+      }
+      logits<MASK>(x[kb], key0 + krow);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, x[kb][i]);
+    }
+    const float m_new = fmaxf(m, half_max(top));
+    const float base = m_new == kNegInf ? 0.f : m_new;      // a row that has seen no key yet
+    const float alpha = __builtin_amdgcn_exp2f(m - base);
+    m = m_new;
+    l = l * alpha;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = o[d][i] * alpha;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const int krow = 32 * (KB * kw + kb);
+      vec p[2];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float e = __builtin_amdgcn_exp2f(x[kb][i] - base);
+        l = l + e;
+        p[i >> 3][i & 7] = static_cast<T>(e);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if constexpr (MASK) {
+          pv_masked(s, krow + 16 * t, key0 + krow + 16 * t, __builtin_bit_cast(v8s, p[t]));
+        } else {
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+            o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v_frag(s, krow + 16 * t, d)), p[t], o[d]);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void run() {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    rl = lane & 31;
+    h = lane >> 5;
+    kw = wave % KW;
+    const int rw = wave / KW;
+    int t = xcd_contiguous(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+    const int rt = t % g.row_tiles;
+    t /= g.row_tiles;
+    const int split = t % g.splits;
+    t /= g.splits;
+    hk = t % g.Hkv;
+    b = t / g.Hkv;
+
+    const int r = (rt * RW + rw) * 32 + rl;
+    const bool real = r < g.rows;
+    const int i = real ? r / g.G : 0;
+    const int head = hk * g.G + (real ? r % g.G : 0);
+    pos = i + g.Lk - g.Lq;
+    slope2 = SLOPES ? g.slopes[head] * kLog2e : 0.f;
+    lo = 0;
+    hi = g.Lk;
+    if (g.ranges != nullptr) {
+      const int32_t* p = g.ranges + b * g.range_b + 2 * static_cast<int64_t>(i);
+      lo = p[0] > 0 ? p[0] : 0;
+      hi = p[1] < hi ? p[1] : hi;
+    }
+    if (g.causal) {
+      const int pre = g.prefix != nullptr ? g.prefix[b] : 0;
+      const int c = pos + 1 > pre ? pos + 1 : pre;
+      hi = c < hi ? c : hi;
+    }
+    if (!real || hi <= lo) {          // sees nothing
+      lo = g.Lk;
+      hi = 0;
+    }
+    // the wave's bounds; rows past the end ask for no mask
+    w_lo = lo;
+    w_hi = hi;
+    w_lo_max = real ? lo : 0;
+    w_hi_min = real ? hi : g.Lk;
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2) {
+      w_lo = min(w_lo, __shfl_xor(w_lo, d));
+      w_hi = max(w_hi, __shfl_xor(w_hi, d));
+      w_lo_max = max(w_lo_max, __shfl_xor(w_lo_max, d));
+      w_hi_min = min(w_hi_min, __shfl_xor(w_hi_min, d));
+    }
+    w_lo = __builtin_amdgcn_readfirstlane(w_lo);
+    w_hi = __builtin_amdgcn_readfirstlane(w_hi);
+    w_lo_max = __builtin_amdgcn_readfirstlane(w_lo_max);
+    w_hi_min = __builtin_amdgcn_readfirstlane(w_hi_min);
+    if (lane == 0) {
+      lds.bounds[wave][0] = w_lo;
+      lds.bounds[wave][1] = w_hi;
+    }
+    __syncthreads();
+    int first = lds.bounds[0][0], last = lds.bounds[0][1];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      first = min(first, lds.bounds[w][0]);
+      last = max(last, lds.bounds[w][1]);
+    }
+    first = __builtin_amdgcn_readfirstlane(first);
+    last = __builtin_amdgcn_readfirstlane(last);
+    // this workgroup's share of the tiles
+    const int tiles = last > first ? (last - first + KT - 1) / KT : 0;
+    const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / g.splits);
+    const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / g.splits);
+
+#pragma unroll
+    for (int c = 0; c < CPW; ++c) {
+      const int row = (CPW * wave + c) * RPC + lane / UNITS;
+      const int unit = (lane % UNITS) ^ (row & (UNITS - 1));
+      const bool in = unit * 8 < g.D;               // D is a multiple of 8
+      koff[c] = in ? static_cast<uint32_t>((row * g.k_l + unit * 8) * 2) : 0xFFFFFFF0u;
+      voff[c] = in ? static_cast<uint32_t>((row * g.v_l + unit * 8) * 2) : 0xFFFFFFF0u;
+    }
+    if (t0 < t1) copy(0, first + t0 * KT, last - (first + t0 * KT));
+
+    const T* qp = static_cast<const T*>(g.q) + b * g.q_b + static_cast<int64_t>(i) * g.q_l +
+                  static_cast<int64_t>(head) * g.q_h;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const int c = (2 * s + h) * 8;
+      v4i z = v4i{0, 0, 0, 0};
+      if (real && c < g.D) z = *reinterpret_cast<const v4i*>(qp + c);
+      qf[s] = __builtin_bit_cast(vec, z);
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+    m = kNegInf;
+    l = 0.f;
+
+    for (int tt = t0; tt < t1; ++tt) {
+      const int key0 = first + tt * KT;
+      const int s = (tt - t0) & 1;
+      __builtin_amdgcn_s_waitcnt(wait_vmem(0));
+      __syncthreads();                 // the tile is in stage s, stage s ^ 1 is free
+      if (tt + 1 < t1) copy(s ^ 1, key0 + KT, last - (key0 + KT));
+      const int k0 = key0 + 32 * KB * kw, k1 = k0 + 32 * KB;   // this wave's keys
+      if (k1 <= w_lo || k0 >= w_hi) continue;
+      if (k0 >= w_lo_max && k1 <= w_hi_min) tile<false>(s, key0);
+      else tile<true>(s, key0);
+    }
+    l = half_sum(l);
+    if constexpr (KW > 1) join_waves();
+    if (KW == 1 || wave == 0) store(real, split, r, i, head);
+  }
+
+  // Adds the partial results of the workgroup's waves, in wave order, into
+  // wave 0: o in fp32 scaled to the common maximum.
+  __device__ __forceinline__ void join_waves() {
+    float* mem = reinterpret_cast<float*>(&lds);
+    float* ml = mem + kWaves * 32 * DP;
+    __syncthreads();                   // the tiles are no longer read
+    if (h == 0) {
+      ml[(wave * 32 + rl) * 2] = m;
+      ml[(wave * 32 + rl) * 2 + 1] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mem[((wave * DB + d) * 16 + e) * 64 + lane] = o[d][e];
+    __syncthreads();
+    if (wave != 0) return;
+    float top = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml[(w * 32 + rl) * 2]);
+    const float base = top == kNegInf ? 0.f : top;
+    float f[kWaves];
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      f[w] = __builtin_amdgcn_exp2f(ml[(w * 32 + rl) * 2] - base);
+      l = __builtin_fmaf(ml[(w * 32 + rl) * 2 + 1], f[w], l);
+    }
+    m = top;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+          v = __builtin_fmaf(mem[((w * DB + d) * 16 + e) * 64 + lane], f[w], v);
+        o[d][e] = v;
+      }
+  }
+
+  __device__ __forceinline__ void store(bool real, int split, int r, int i, int head) {
+    if (!real) return;
+    if (g.splits > 1) {
+      const int64_t row = ((static_cast<int64_t>(split) * g.B + b) * g.Hkv + hk) * g.rows + r;
+      if (h == 0) {
+        g.part_ml[2 * row] = m;
+        g.part_ml[2 * row + 1] = l;
+      }
+      if (l == 0.f) return;            // the join reads no outputs of such a row
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int ch = 32 * d + 8 * e + 4 * h;
+          if (ch < g.D)
+            *reinterpret_cast<v4f*>(g.part_o + row * g.D + ch) =
+                v4f{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+        }
+      return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    T* op = static_cast<T*>(g.out) + b * g.o_b + static_cast<int64_t>(i) * g.o_l +
+            static_cast<int64_t>(head) * g.o_h;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int ch = 32 * d + 8 * e + 4 * h;
+        if (ch < g.D) {
+          typedef T vec4 __attribute__((ext_vector_type(4)));
+          vec4 y;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) y[c] = static_cast<T>(o[d][4 * e + c] * inv);
+          *reinterpret_cast<vec4*>(op + ch) = y;
+        }
+      }
+  }
+};
+
+template <class T, int DP, int RW, bool CAP, bool SLOPES>
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(const AttnArgs g) {
+  using A = Attention<T, DP, RW, CAP, SLOPES>;
+  __shared__ typename A::Lds lds;
+  A a(g, lds);
+  a.run();
+}
+
+// Joins the splits of one output row per 16 lanes: 8 channels per lane.
+template <class T>
+__global__ __launch_bounds__(256) void attention_join(const AttnArgs g) {
+  const int64_t all = static_cast<int64_t>(g.B) * g.Hkv * g.rows;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
+  const int ch = 8 * (threadIdx.x % 16);
+  if (row >= all || ch >= g.D) return;
+  float top = kNegInf;
+  for (int s = 0; s < g.splits; ++s) top = fmaxf(top, g.part_ml[2 * (s * all + row)]);
+  const float base = top == kNegInf ? 0.f : top;
+  float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < g.splits; ++s) {
+    const float ls = g.part_ml[2 * (s * all + row) + 1];
+    if (ls == 0.f) continue;
+    const float f = __builtin_amdgcn_exp2f(g.part_ml[2 * (s * all + row)] - base);
+    l = __builtin_fmaf(ls, f, l);
+    const float* p = g.part_o + (s * all + row) * g.D + ch;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(p[e], f, o[e]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const int64_t r = row % g.rows, bh = row / g.rows;
+  const int64_t b = bh / g.Hkv, hk = bh % g.Hkv;
+  T* op = static_cast<T*>(g.out) + b * g.o_b + (r / g.G) * g.o_l + (hk * g.G + r % g.G) * g.o_h + ch;
+  typedef T vec8 __attribute__((ext_vector_type(8)));
+  vec8 y;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = static_cast<T>(o[e] * inv);
+  *reinterpret_cast<vec8*>(op) = y;
+}
+
+template <class T, int DP, int RW, bool CAP>
+void launch_s(const AttnArgs& g, unsigned grid, hipStream_t stream) {
+  if (g.slopes != nullptr)
+    hipLaunchKernelGGL((attention_kernel<T, DP, RW, CAP, true>), dim3(grid), dim3(64 * kWaves), 0,
+                       stream, g);
+  else
+    hipLaunchKernelGGL((attention_kernel<T, DP, RW, CAP, false>), dim3(grid), dim3(64 * kWaves), 0,
+                       stream, g);
+}
+
+template <class T, int DP, int RW>
+void launch_c(const AttnArgs& g, unsigned grid, hipStream_t stream) {
+  g.cap2 != 0.f ? launch_s<T, DP, RW, true>(g, grid, stream)
+                : launch_s<T, DP, RW, false>(g, grid, stream);
+}
+
+template <class T>
+hipError_t launch_t(const AttnArgs& g, const AttnPlan& p, hipStream_t stream) {
+  if (p.few)
+    g.D > 64 ? launch_c<T, 128, 1>(g, p.grid, stream) : launch_c<T, 64, 1>(g, p.grid, stream);
+  else
+    g.D > 64 ? launch_c<T, 128, 4>(g, p.grid, stream) : launch_c<T, 64, 4>(g, p.grid, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || g.splits == 1) return e;
+  const int64_t rows = static_cast<int64_t>(g.B) * g.Hkv * g.rows;
+  hipLaunchKernelGGL(attention_join<T>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0,
+                     stream, g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+AttnPlan attention_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, bool split) {
+  AttnPlan p{};
+  const int64_t rows = Lq * (Hq / Hkv);
+  p.few = rows <= 32;
+  p.row_tiles = (rows + (p.few ? 31 : 127)) / (p.few ? 32 : 128);
+  const int64_t wgs = p.row_tiles * B * Hkv;
+  int64_t s = 1;
+  if (split) {
+    s = resident_slots() / (wgs > 0 ? wgs : 1);
+    const int64_t most = Lk / 256;      // at least 256 keys per workgroup
+    s = s > most ? most : s;
+    s = s < 1 ? 1 : s > 64 ? 64 : s;
+  }
+  p.splits = static_cast<int>(s);
+  p.wgs = wgs * s;
+  p.grid = static_cast<unsigned>(p.wgs);
+  return p;
+}
+
+hipError_t launch_attention(AttnArgs g, int dtype, const AttnPlan& p, hipStream_t stream) {
+  g.row_tiles = static_cast<int>(p.row_tiles);
+  g.splits = p.splits;
+  return dtype == SVDQ_F16 ? launch_t<_Float16>(g, p, stream) : launch_t<__bf16>(g, p, stream);
+}
+
+}  // namespace svdq

@@ -1,0 +1,41 @@
+// Host-side launcher of the attention kernels (abi_block.hip validates every
+// argument before it calls them).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace svdq {
+
+// Strides in elements: _b batch, _l token, _h head; channels are contiguous.
+struct AttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  int64_t q_b, q_l, q_h, k_b, k_l, k_h, v_b, v_l, v_h, o_b, o_l, o_h;
+  const float* slopes;       // per query head, or null
+  const int32_t* prefix;     // per batch entry, or null
+  const int32_t* ranges;     // [begin, end) per query row, or null
+  int64_t range_b;           // batch stride of ranges (elements; 0: shared)
+  float* part_ml;            // splits: maximum and sum per row
+  float* part_o;             // splits: unnormalized outputs, D per row
+  float scale2;              // scale * log2(e)
+  float cap_in, cap2;        // 2 log2(e) scale / cap, cap * log2(e); cap2 0: no cap
+  int B, Lq, Lk, Hkv, G, D;  // G query heads per key head
+  int rows;                  // Lq * G
+  int causal;
+  int row_tiles, splits;     // set by launch_attention
+};
+
+struct AttnPlan {
+  bool few;                  // at most 32 rows per key head: waves split the keys
+  int64_t row_tiles, wgs;
+  int splits;                // workgroups along the keys
+  unsigned grid;
+};
+
+AttnPlan attention_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, bool split);
+hipError_t launch_attention(AttnArgs g, int dtype, const AttnPlan& p, hipStream_t stream);
+
+}  // namespace svdq

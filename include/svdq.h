@@ -87,8 +87,9 @@ enum {
   SVDQ_ERR_ACT = 11        /* unknown activation code */
 };
 
-/* dtype codes for X and Y */
-enum { SVDQ_F16 = 1, SVDQ_F32 = 2 };
+/* dtype codes for X and Y. SVDQ_BF16 is taken by the 8-bit attention block's
+ * entry points only; the others return SVDQ_ERR_DTYPE for it. */
+enum { SVDQ_F16 = 1, SVDQ_F32 = 2, SVDQ_BF16 = 3 };
 
 /* Activation applied by K2's epilogue to the fp32 result before its one
  * rounding to the output type. GELU is the tanh form between the two linears
@@ -100,6 +101,8 @@ enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU_TANH = 1 };
 #define SVDQ_GROUP 64
 /* Values per shared scale in the MXFP4 format. */
 #define SVDQ_MX_BLOCK 32
+/* Channels per scale in the 8-bit (e4m3) format. */
+#define SVDQ_FP8_BLOCK 128
 /* Largest rank the device kernels accept. */
 #define SVDQ_MAX_RANK 256
 
@@ -648,6 +651,101 @@ int svdq_debug_group_partials(const uint8_t* a_codes, const uint8_t* w_codes, in
  * textbook formula 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))), computed
  * in fp32 from fp16 and rounded to fp16. x and y may be the same buffer. */
 int svdq_gelu_tanh_f16(const uint16_t* x, uint16_t* y, int64_t n, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit attention block: the operators around the quantized linears of a
+ * transformer block, and an 8-bit linear for the layers that a 4-bit model
+ * keeps at higher precision (not on the pages; each is stated by its formula).
+ *
+ * The 8-bit format: OCP e4m3 codes (1 byte, largest finite value 448, NaN
+ * 0x7F/0xFF) with fp32 scales, Kp = K rounded up to 128, G = Kp / 128.
+ *   a_codes: M x Kp, a_scales: M x G (one scale per row and 128 channels);
+ *   w_codes: N x Kp, w_scales: ceil(N/128) x G (one per 128 x 128 block).
+ * Codes of channels K .. Kp-1 are 0. Quantizer of a group v (a row's 128
+ * channels, or a weight block):
+ *   a = max|v|; s = max(fp32(a / 448), 2^-126); q = e4m3_rne(fp32(v * fp32(1/s))).
+ * A NaN quantizes to the NaN code and an infinity too (its group's other codes
+ * are 0 and its scale infinite), so neither is lost.
+ *
+ * Rows are row-major with unit inner stride and any row stride; X, residual and
+ * residual_out need only the alignment of their element type. M = 0 (and for
+ * attention B or Lq = 0) is a call that does nothing.
+ */
+
+/* Host: W (K x N row-major fp32, Y = X . W) -> w_codes, w_scales. */
+int svdq_prepare_weights_fp8(const float* W, int64_t K, int64_t N, uint8_t* w_codes,
+                             float* w_scales);
+
+/* Device: residual addition, RMS norm and quantization in one pass:
+ *   h = x + residual (fp32; h = x without one); residual_out = round(h);
+ *   u = h / sqrt(mean(h^2) + eps) * gain (1 without one); codes, scales of u.
+ * The norm uses the unrounded h. dtype (f16, bf16, f32) is that of X, residual
+ * and residual_out; gain is K fp32 values (16-byte aligned). residual,
+ * residual_out and gain may be NULL; residual_out may be X or residual itself
+ * with the same row stride, and may not overlap them otherwise. K <= 2^22. */
+int svdq_rmsnorm_quantize_fp8(const void* X, const void* residual, int dtype, int64_t M, int64_t K,
+                              int64_t ldx, int64_t ldr, const float* gain, float eps,
+                              uint8_t* a_codes, float* a_scales, void* residual_out, int64_t ldo,
+                              hipStream_t stream);
+
+/* Device: the quantizer alone, codes and scales of X. */
+int svdq_quantize_act_fp8(const void* X, int dtype, int64_t M, int64_t K, int64_t ldx,
+                          uint8_t* a_codes, float* a_scales, hipStream_t stream);
+
+/* Bytes of the fp32 partial tiles of a product that is split along K on the
+ * current device (0: this shape is not split). */
+size_t svdq_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t Kp);
+
+/* Device: Y[m][n] = act(sum_g a_scales[m][g] * w_scales[n/128][g] *
+ * sum_{k in g} a[m][k] * w[n][k] + bias[n]). Y is f16, bf16 or f32; bias is N
+ * fp32 values or NULL. Codes 16-byte aligned, Kp a multiple of 128 up to 2^22.
+ * Sums across groups are fp32. For f16 and bf16 outputs the sum inside a group
+ * is the 8-bit matrix instruction's (relative error 1e-5 to 5e-5, below the
+ * output's rounding); for f32 outputs it is exact to fp32 rounding. ws: NULL or
+ * a 16-byte aligned workspace; with at least svdq_gemm_fp8_workspace_bytes
+ * bytes a shape with few tiles and long K is split along K. */
+int svdq_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
+                  const float* w_scales, const float* bias, void* Y, int y_dtype, int64_t M,
+                  int64_t N, int64_t Kp, int64_t ldy, int32_t activation, void* ws,
+                  size_t ws_bytes, hipStream_t stream);
+
+/* Device: the 8-bit linear layer, svdq_quantize_act_fp8 into `ws`, then
+ * svdq_gemm_fp8. ws: 256-byte aligned, at least
+ * svdq_linear_fp8_workspace_bytes(M, K, N) bytes. */
+size_t svdq_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t N);
+int svdq_linear_fp8(const void* X, int x_dtype, int64_t ldx, const uint8_t* w_codes,
+                    const float* w_scales, const float* bias, void* Y, int y_dtype, int64_t ldy,
+                    int64_t M, int64_t K, int64_t N, void* ws, size_t ws_bytes,
+                    int32_t activation, hipStream_t stream);
+
+/* Bytes of the partial outputs of an attention that is split along the keys
+ * on the current device (0: this shape is not split). */
+size_t svdq_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv,
+                                      int64_t D);
+
+/* Device: masked attention with grouped heads.
+ *   x[i][j] = scale * q_i . k_j; with softcap > 0: x = softcap * tanh(x / softcap);
+ *   with slopes: x -= slopes[h] * |pos_i - j|, pos_i = i + Lk - Lq;
+ *   out_i = sum_j softmax_j(x[i][j]) v_j over the keys j that row i sees:
+ *   key_ranges (NULL, or [begin, end) int32 pairs per batch entry and query;
+ *   values outside 0 .. Lk are cut) and, if causal, j <= pos_i or j < prefix[b]
+ *   (prefix: NULL or one int32 per batch entry; only with causal).
+ * A row that sees no key is 0; a key that a row does not see does not reach its
+ * output even where its K or V hold infinities or NaN.
+ * dtype (f16, bf16) is that of Q, K, V and Out. Query head h reads key head
+ * h / (Hq / Hkv). `strides`: 12 element strides, (batch, token, head) of Q, K, V
+ * and Out in that order; channels are contiguous. Each is a multiple of 8 and
+ * each pointer 16-byte aligned; token strides of K and V are at most 2^22, and
+ * at least D where Lk > 1. D: a multiple of 8 up to 128. key_ranges_batch:
+ * elements between the ranges of two batch entries (0: shared). Out may not
+ * overlap the inputs. ws: NULL or a 16-byte aligned workspace; with at least
+ * svdq_attention_workspace_bytes bytes few rows over many keys are split along
+ * the keys. */
+int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int dtype, int64_t B,
+                   int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D,
+                   const int64_t* strides, float scale, float softcap, const float* slopes,
+                   int32_t causal, const int32_t* prefix, const int32_t* key_ranges,
+                   int64_t key_ranges_batch, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement utilities (not part of the method): the shader clock during a
