@@ -7,8 +7,9 @@ All checks and all arithmetic are done by the library.
 """
 from __future__ import annotations
 
-import ctypes
 import dataclasses
+import functools
+import struct
 from typing import Optional
 
 import numpy as np
@@ -254,7 +255,9 @@ def concat_lora(prep: Prepared, lam: np.ndarray, A: np.ndarray, B: np.ndarray,
 
 
 def _torch():
-    import torch
+    torch = _lib.torch
+    if torch is None:
+        raise ImportError("the device entry points take torch tensors: torch is not installed")
     return torch
 
 
@@ -263,9 +266,17 @@ def _tp(t):
 
 
 def _stream(stream):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    """Raw handle of the given stream, or of torch's current one on the current device.
+
+    torch.cuda.current_stream() builds a Stream object (2.7 us, as long as a kernel
+    launch); the raw handle alone costs 0.1 us."""
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch()._C
+    try:
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    except AttributeError:                        # a torch without these names
+        return _torch().cuda.current_stream().cuda_stream
 
 
 def _dt(t) -> int:
@@ -287,9 +298,25 @@ def _dtname(t) -> str:
     return str(t.dtype).replace("torch.", "")
 
 
+# The checks run on every call and a small layer's kernel takes no longer than
+# they do, so each first tests the whole of what it requires with the cheapest
+# accessors, and only a tensor that fails goes through the tests one by one to
+# find the message.
+
+@functools.lru_cache(maxsize=None)
+def _dtypes(names):
+    torch = _torch()
+    return frozenset(getattr(torch, n) for n in names if hasattr(torch, n))
+
+
 def _buf(name, t, dtypes, nbytes=None, min_bytes=None, contiguous=True):
     """A flat buffer: dtype in `dtypes`, exactly `nbytes` or at least `min_bytes`."""
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.dtype in _dtypes(dtypes):
+        size = t.nbytes
+        if (nbytes is None or size == nbytes) and (min_bytes is None or size >= min_bytes) and (
+                not contiguous or t.is_contiguous()):
+            return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
     if _dtname(t) not in dtypes:
@@ -307,6 +334,13 @@ def _buf(name, t, dtypes, nbytes=None, min_bytes=None, contiguous=True):
 def _mat(name, t, rows, cols, dtypes=_XY):
     """A row-major matrix of `rows` x `cols` with unit inner stride (any row stride >= cols)."""
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.dtype in _dtypes(dtypes):
+        shape = t.shape
+        if len(shape) == 2:
+            r, c = shape
+            sr, sc = t.stride()
+            if (rows is None or r == rows) and (cols is None or c == cols) and sc == 1 and sr >= c:
+                return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
     if _dtname(t) not in dtypes:
@@ -322,6 +356,16 @@ def _mat(name, t, rows, cols, dtypes=_XY):
 
 
 def _on_gpu(*ts):
+    first = None
+    for t in ts:
+        if t is not None:
+            d = t.get_device()                    # -1 on the CPU
+            if first is None:
+                first = d
+            if d < 0 or d != first or not t.is_cuda:
+                break
+    else:
+        return
     devs = {(t.device.type, t.device.index) for t in ts if t is not None}
     if any(d[0] != "cuda" for d in devs):
         raise ValueError("every tensor must be on a GPU (device memory)")
@@ -1015,6 +1059,7 @@ def attention_workspace_bytes(B: int, Lq: int, Lk: int, Hq: int, Hkv: int, D: in
 
 
 def _heads(name, t, B, L, H, D, dtype):
+    """Batch, token and head strides of a B x L x H x D tensor (None: any size)."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
@@ -1027,7 +1072,13 @@ def _heads(name, t, B, L, H, D, dtype):
     if t.shape[3] > 1 and t.stride(3) != 1:
         raise ValueError(f"{name}: the inner stride must be 1, got {t.stride(3)}")
     # a dimension of one (or of none) is never stepped over: its stride is free
-    return [t.stride(i) if t.shape[i] > 1 else t.shape[3] if i == 1 else 0 for i in range(3)]
+    sb, sl, sh, _ = t.stride()
+    if t.numel() and (t.shape[0] == 1 or t.shape[1] == 1 or t.shape[2] == 1):
+        b, l, h, d = t.shape
+        sb, sl, sh = sb if b > 1 else 0, sl if l > 1 else d, sh if h > 1 else 0
+    elif not t.numel():
+        sb, sl, sh = 0, t.shape[3], 0
+    return sb, sl, sh
 
 
 def attention(Q, K, V, Out, scale: float | None = None, softcap: float = 0.0, slopes=None,
@@ -1066,7 +1117,7 @@ def attention(Q, K, V, Out, scale: float | None = None, softcap: float = 0.0, sl
     if ws is not None:
         _buf("ws", ws, _BYTES + _HALF + _F32)
     _on_gpu(Q, K, V, Out, slopes, prefix, key_ranges, ws)
-    strides = (ctypes.c_int64 * 12)(*sq_, *sk, *sv, *so)
+    strides = struct.pack("12q", *sq_, *sk, *sv, *so)
     check(lib.svdq_attention(
         _tp(Q), _tp(K), _tp(V), _tp(Out), _dt_block(Q), B, Lq, Lk, Hq, Hkv, D, strides,
         D ** -0.5 if scale is None else float(scale), float(softcap), _tp(slopes),
