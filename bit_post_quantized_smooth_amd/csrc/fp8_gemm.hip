@@ -39,6 +39,7 @@ namespace svdq {
 namespace {
 
 constexpr int kChunk = kFp8Block;   // K values per group and matrix instruction
+constexpr int kWaitAll = 0x0070;    // vmcnt(0) expcnt(7) lgkmcnt(0)
 
 struct GemmArgs {
   const uint8_t* a;
@@ -103,20 +104,34 @@ __device__ __forceinline__ v4f bias4(const GemmArgs& g, int64_t n) {
   return b;
 }
 
-// Columns n .. n+3 of row m of Y (of type YT) from the fp32 sums v: the bias,
-// the optional GELU, one rounding, one store where Y's alignment allows it.
+// The bias, the optional GELU and the one rounding to a 16-bit output.
+template <int YT, bool GELU>
+__device__ __forceinline__ uint2 round4(v4f v, v4f b) {
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x = v[e] + b[e];
+    if constexpr (GELU) x = gelu_tanh_f32(x);
+    if constexpr (YT == SVDQ_F16) h[e] = f2h(x);
+    else h[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+  }
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// Columns n .. n+3 of row m of Y (of type YT) from the fp32 sums v, in one
+// store where Y's alignment allows it.
 template <int YT, bool GELU>
 __device__ __forceinline__ void finish4(const GemmArgs& g, v4f v, v4f b, int64_t m, int64_t n) {
   if (m >= g.M || n >= g.N) return;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = v[e] + b[e];
-    if constexpr (GELU) v[e] = gelu_tanh_f32(v[e]);
-  }
   constexpr int ES = YT == SVDQ_F32 ? 4 : 2;
   const bool vec =
       n + 3 < g.N && ((reinterpret_cast<uintptr_t>(g.Y) | (g.ldy * ES)) % (4 * ES)) == 0;
   if constexpr (YT == SVDQ_F32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = v[e] + b[e];
+      if constexpr (GELU) v[e] = gelu_tanh_f32(v[e]);
+    }
     float* y = static_cast<float*>(g.Y) + m * g.ldy + n;
     if (vec) {
       *reinterpret_cast<v4f*>(y) = v;
@@ -126,21 +141,14 @@ __device__ __forceinline__ void finish4(const GemmArgs& g, v4f v, v4f b, int64_t
         if (n + e < g.N) y[e] = v[e];
     }
   } else {
-    uint16_t h[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = v[e];
-      if constexpr (YT == SVDQ_F16) h[e] = f2h(x);
-      else h[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
-    }
+    const uint2 h = round4<YT, GELU>(v, b);
     uint16_t* y = static_cast<uint16_t*>(g.Y) + m * g.ldy + n;
     if (vec) {
-      *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16),
-                                                h[2] | (static_cast<uint32_t>(h[3]) << 16));
+      *reinterpret_cast<uint2*>(y) = h;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (n + e < g.N) y[e] = h[e];
+        if (n + e < g.N) y[e] = static_cast<uint16_t>((e < 2 ? h.x : h.y) >> (16 * (e & 1)));
     }
   }
 }
@@ -244,33 +252,113 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
     return f;
   };
 
-  if (c0 < c1) copy(0, c0);
+  // Software pipeline. While row block i's products go out, the products of
+  // the block before it are added (two sets of partials), and block i+1 is read
+  // (two sets of activation operands); each matrix instruction is followed by
+  // the four additions of one issued NBN instructions earlier. The last block of
+  // a chunk needs nothing more from its stage, so the barrier stands before it:
+  // behind it go the copies of chunk c+2 into the stage just read, and the first
+  // operands of chunk c+1, which the copies of the chunk before have brought.
+  static_assert(NBM % 2 == 0, "the operand sets alternate across chunks too");
+  Frag<EXACT> fw[NBN], fa[2];
+  v4f p[2][NBN];
+  float raw[2] = {0.f, 0.f}, sw = 0.f, sw_prev = 0.f;
+#pragma unroll
+  for (int j = 0; j < NBN; ++j) p[1][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto scale_of = [&](int i, int c) {
+    return sal[((c - c0) >> 2) & 1][(wm * NBM + i) * 16 + rl][(c - c0) & 3];
+  };
+  auto wait_all = [&]() {              // this wave's copies and LDS reads, then every wave's
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    __builtin_amdgcn_s_barrier();
+  };
+  swv = c0 + lane < c1 ? swp[c0 + lane] : 0.f;
+  copy(0, c0);
+  if (c0 + 1 < c1) copy(1, c0 + 1);
+  wait_all();
+  fa[0] = frag(st[0].a, wm * NBM);
+  float next_raw = scale_of(0, c0);
+#pragma unroll
+  for (int j = 0; j < NBN; ++j) fw[j] = frag(st[0].w, wn * NBN + j);
   for (int c = c0; c < c1; ++c) {
     const int s = (c - c0) & 1;
-    if (((c - c0) & 63) == 0) swv = c + lane < c1 ? swp[c + lane] : 0.f;
-    __builtin_amdgcn_s_waitcnt(wait_vmem(0));
-    __syncthreads();                       // chunk c is in stage s; stage s ^ 1 is free
-    if (c + 1 < c1) copy(s ^ 1, c + 1);
-    const float sw = __builtin_bit_cast(
+    sw_prev = sw;
+    sw = __builtin_bit_cast(
         float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, swv), (c - c0) & 63));
-    const float(*sc)[4] = sal[((c - c0) >> 2) & 1];
-    Frag<EXACT> fw[NBN];
-#pragma unroll
-    for (int j = 0; j < NBN; ++j) fw[j] = frag(st[s].w, wn * NBN + j);
 #pragma unroll
     for (int i = 0; i < NBM; ++i) {
-      const Frag<EXACT> fa = frag(st[s].a, wm * NBM + i);
-      const float scale = sc[(wm * NBM + i) * 16 + rl][(c - c0) & 3] * sw;
+      raw[i & 1] = next_raw;
+      if (i + 1 < NBM) {
+        fa[(i + 1) & 1] = frag(st[s].a, wm * NBM + i + 1);
+        next_raw = scale_of(i + 1, c);
+      } else {
+        if (((c - c0) & 63) == 63) swv = c + 1 + lane < c1 ? swp[c + 1 + lane] : 0.f;
+        wait_all();
+        if (c + 2 < c1) copy(s, c + 2);
+        fa[0] = frag(st[s ^ 1].a, wm * NBM);
+        next_raw = scale_of(0, c + 1);
+      }
+      // the scale of the products added here: row block i-1 of this chunk, or
+      // the last block of the chunk before
+      const float scale = raw[(i + 1) & 1] * (i > 0 ? sw : sw_prev);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < NBN; ++j) {
-        const v4f p = mfma_group(fw[j], fa);
+        p[i & 1][j] = mfma_group(fw[j], fa[i & 1]);
+        if (i + 1 == NBM) fw[j] = frag(st[s ^ 1].w, wn * NBN + j);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], scale, acc[i][j][e]);
+        for (int e = 0; e < 4; ++e) {
+          const int d = (i + NBM - 1) % NBM;
+          acc[d][j][e] = __builtin_fmaf(p[(i + 1) & 1][j][e], scale, acc[d][j][e]);
+        }
+        // the sums are made here: without this the compiler moves them past the
+        // branches below and keeps every partial of the chunk until then
+        asm volatile("" : "+v"(acc[(i + NBM - 1) % NBM][j]));
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
+  {
+    const float scale = raw[1] * sw;
+#pragma unroll
+    for (int j = 0; j < NBN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[NBM - 1][j][e] = __builtin_fmaf(p[1][j][e], scale, acc[NBM - 1][j][e]);
+  }
 
   const int64_t mw = m0 + wm * NBM * 16 + rl, nw = n0 + wn * NBN * 16 + 4 * q;
+  // A 16-bit Y goes out through the wave's share of the stages, where a row's
+  // 64 columns make one 128-byte line: 8 lanes store a whole line, instead of 4
+  // lanes a 32-byte piece of it.
+  if constexpr (YT != SVDQ_F32 && NBN == 4) {
+    static_assert(sizeof(st) >= static_cast<size_t>(T::NW) * NBM * 16 * 128, "room for the tile");
+    __syncthreads();                   // the last operands read ahead are not needed
+    const int64_t n_wave = n0 + wn * 64;
+    if (g.slices == 1 && n_wave + 64 <= g.N &&
+        ((reinterpret_cast<uintptr_t>(g.Y) | (g.ldy * 2)) & 15) == 0) {
+      uint8_t* mem = reinterpret_cast<uint8_t*>(&st) + wave * NBM * 16 * 128;
+#pragma unroll
+      for (int j = 0; j < NBN; ++j) {
+        const v4f b = bias4(g, nw + 16 * j);
+#pragma unroll
+        for (int i = 0; i < NBM; ++i) {
+          const int row = 16 * i + rl, u = (2 * j + (q >> 1)) ^ (row & 7);
+          *reinterpret_cast<uint2*>(mem + row * 128 + u * 16 + (q & 1) * 8) =
+              round4<YT, GELU>(acc[i][j], b);
+        }
+      }
+      const int64_t m_wave = m0 + wm * NBM * 16;
+      uint16_t* y = static_cast<uint16_t*>(g.Y) + n_wave + 8 * (lane & 7);
+#pragma unroll
+      for (int t = 0; t < 2 * NBM; ++t) {
+        const int row = 8 * t + r8;
+        const v4i v = *reinterpret_cast<const v4i*>(mem + row * 128 + (((lane & 7) ^ r8) << 4));
+        if (m_wave + row < g.M) *reinterpret_cast<v4i*>(y + (m_wave + row) * g.ldy) = v;
+      }
+      return;
+    }
+  }
   if (g.slices == 1) {
 #pragma unroll
     for (int j = 0; j < NBN; ++j) {
@@ -408,7 +496,8 @@ hipError_t launch_e(GemmArgs& g, hipStream_t stream) {
   const int64_t big = ((g.M + 255) / 256) * ((g.N + 255) / 256);
   if (big >= resident_slots() / 4) {
     g.slices = 1;
-    launch_tiles<2, 4, 8, 4, YT, GELU>(g, stream);
+    // an fp32 output's operands take twice the registers
+    launch_tiles<2, 4, YT == SVDQ_F32 ? 4 : 8, 4, YT, GELU>(g, stream);
     return hipGetLastError();
   }
   g.slices = g.part != nullptr ? split_slices(g.M, g.N, g.Kp) : 1;
