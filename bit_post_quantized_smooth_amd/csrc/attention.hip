@@ -143,6 +143,15 @@ struct Attention {
       buffer_to_lds16(bv, &lds.v[s][(CPW * wave + i) * RPC][0], voff[i], 0);
   }
 
+  // Unit u of row r lies at u ^ twist(r). LDS has 64 banks of 4 bytes. A read of
+  // the K operand takes one unit of 16 consecutive rows at a time, one of V^T 64
+  // bytes of 4 consecutive rows (starting at a multiple of 4): the twist has to
+  // differ in all of 16 rows (rows of 256 bytes) or in 8 of one parity (128
+  // bytes), and in its bit of 64 bytes between rows that share banks among 4.
+  static __device__ __forceinline__ int twist(int r) {
+    return UNITS == 16 ? 4 * (r & 3) + ((r >> 2) & 3) : 2 * (r & 2) + ((r >> 2) & 3);
+  }
+
   // The V^T operand of 16 keys (from key on) and output block d: lane (d, h)
   // gets keys 4h .. 4h+3 and 8+4h .. 8+4h+3 of channel 32 d + lane % 32.
   __device__ __forceinline__ v8s v_frag(int s, int key, int d) {
@@ -152,7 +161,7 @@ struct Attention {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int row = key + 8 * e + 4 * (g16 >> 1) + (a >> 2);
-      const int unit = (ch >> 3) ^ (row & (UNITS - 1));
+      const int unit = (ch >> 3) ^ twist(row);
       const uint8_t* p = &lds.v[s][row][unit * 16 + (ch & 4) * 2];
       part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (__attribute__((address_space(3))) v4s*)(p));
@@ -238,7 +247,7 @@ struct Attention {
       const int row = krow + rl;
 #pragma unroll
       for (int t = 0; t < DS; ++t) {
-        const int unit = (2 * t + h) ^ (row & (UNITS - 1));
+        const int unit = (2 * t + h) ^ twist(row);
         const v4i kf = *reinterpret_cast<const v4i*>(&lds.k[s][row][unit * 16]);
         x[kb] = Half<T>::mfma(__builtin_bit_cast(vec, kf), qf[t], x[kb]);
       }
@@ -352,7 +361,7 @@ struct Attention {
 #pragma unroll
     for (int c = 0; c < CPW; ++c) {
       const int row = (CPW * wave + c) * RPC + lane / UNITS;
-      const int unit = (lane % UNITS) ^ (row & (UNITS - 1));
+      const int unit = (lane % UNITS) ^ twist(row);
       const bool in = unit * 8 < g.D;               // D is a multiple of 8
       koff[c] = in ? static_cast<uint32_t>((row * g.k_l + unit * 8) * 2) : 0xFFFFFFF0u;
       voff[c] = in ? static_cast<uint32_t>((row * g.v_l + unit * 8) * 2) : 0xFFFFFFF0u;

@@ -21,13 +21,15 @@
 // Three kernels:
 // - tiles: a workgroup computes BM x BN outputs, both operands copied from
 //   global memory straight into LDS, one 128-byte row piece per row and chunk,
-//   its 16-byte units XOR-swizzled by row % 8 so that the operand reads of 8
-//   lanes cover all banks. Optionally split along K, each slice writing fp32
-//   partial tiles, which a second kernel adds in slice order.
-// - few rows (M <= 64): bound by reading the weights once. A workgroup owns 16
+//   its 16-byte units XOR-swizzled so that the operand reads of 16 lanes cover
+//   all banks. Optionally split along K, each slice writing fp32 partial tiles.
+// - few rows (M <= 16): bound by reading the weights once. A workgroup owns 16
 //   columns, its waves take the groups in turn, operands go straight to
 //   registers, and the waves' accumulators are added through LDS in order.
+// - the sums of a product split along K, in slice order.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "../../include/svdq.h"
 #include "block_common.hpp"
@@ -39,7 +41,8 @@ namespace svdq {
 namespace {
 
 constexpr int kChunk = kFp8Block;   // K values per group and matrix instruction
-constexpr int kWaitAll = 0x0070;    // vmcnt(0) expcnt(7) lgkmcnt(0)
+// vmcnt(n) expcnt(7) lgkmcnt(0)
+constexpr int wait_copies(int n) { return (n & 15) | ((n >> 4) << 14) | 0x70; }
 
 struct GemmArgs {
   const uint8_t* a;
@@ -52,6 +55,14 @@ struct GemmArgs {
   int64_t M, N, Kp, ldy;
   int slices;
 };
+
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
 
 __device__ __forceinline__ v8h widen8(int lo, int hi) {
   const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
@@ -154,30 +165,33 @@ __device__ __forceinline__ void finish4(const GemmArgs& g, v4f v, v4f b, int64_t
 }
 
 // ---------------------------------------------------------------------------
-// Tiles
+// Tiles: WM x WN waves, each of 16*NBM rows and 16*NBN columns; NST chunks in
+// LDS. Two stages are all that fits with a large tile, whose chunk takes longer
+// than its copies; a small tile's chunk does not, so four are in flight.
 
-template <int WM, int WN, int NBM, int NBN>
+template <int WM, int WN, int NBM, int NBN, int NST>
 struct Tile {
-  static constexpr int BM = WM * NBM * 16, BN = WN * NBN * 16, NW = WM * WN;
+  static constexpr int NW = WM * WN, BM = WM * NBM * 16, BN = WN * NBN * 16;
   struct alignas(16) Stage {
     uint8_t a[BM][kChunk];
     uint8_t w[BN][kChunk];
   };
   struct Lds {
-    Stage st[2];
+    Stage st[NST];
     alignas(16) float sal[2][BM][4];   // activation scales of 4 groups
   };
-  // one 1 KB copy instruction moves 8 rows of 128 bytes
-  static constexpr int CA = BM / 8 / NW, CW = BN / 8 / NW;
-  static_assert(CA * 8 * NW == BM && CW * 8 * NW == BN, "whole copy instructions per wave");
+  // one 1 KB copy instruction moves 8 rows of 128 bytes; wave w takes every
+  // NW-th, the last of them where there is one
+  static constexpr int CA = BM / 8 / NW, CW = (BN / 8 + NW - 1) / NW;
+  static_assert(CA * 8 * NW == BM && BN % 16 == 0, "whole copy instructions");
   static_assert(BM % 64 == 0 && BM / 64 <= NW, "one scale copy per wave at most");
 };
 
-template <int WM, int WN, int NBM, int NBN, int YT, bool GELU>
+template <int WM, int WN, int NBM, int NBN, int NST, int YT, bool GELU>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g, int tiles_m,
                                                                int tiles_n) {
   constexpr bool EXACT = YT == SVDQ_F32;
-  using T = Tile<WM, WN, NBM, NBN>;
+  using T = Tile<WM, WN, NBM, NBN, NST>;
   // one object: with two, the compiler tags copies and reads with the object
   // they belong to and makes every read wait for every copy in flight
   __shared__ typename T::Lds lds;
@@ -201,42 +215,66 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
   // Rows past the end are clamped to the last one; their results are dropped.
   const int rows_a = static_cast<int>(g.M - m0 < T::BM ? g.M - m0 : T::BM);
   const int rows_w = static_cast<int>(g.N - n0 < T::BN ? g.N - n0 : T::BN);
-  const __amdgpu_buffer_rsrc_t ba = make_buffer(g.a + m0 * g.Kp, static_cast<uint32_t>(rows_a * g.Kp));
-  const __amdgpu_buffer_rsrc_t bw = make_buffer(g.w + n0 * g.Kp, static_cast<uint32_t>(rows_w * g.Kp));
-  const __amdgpu_buffer_rsrc_t bs = make_buffer(g.sa + m0 * C, static_cast<uint32_t>(rows_a * C * 4));
-  const int r8 = lane >> 3, unit = (lane & 7) ^ r8;
+  const __amdgpu_buffer_rsrc_t bs =
+      make_buffer(g.sa + m0 * C, static_cast<uint32_t>(rows_a * C * 4));
+  // position of row r's 16-byte unit u in LDS: u ^ ((r >> 1) & 7); an even and
+  // an odd row lie in different halves of the 64 banks
+  const int r8 = lane >> 3, unit = (lane & 7) ^ (4 * (wave & 1) + (r8 >> 1));
+  static_assert(T::NW % 2 == 0, "a copy's rows start at 8 * wave, up to multiples of 16");
   uint32_t oa[T::CA], ow[T::CW];
 #pragma unroll
   for (int i = 0; i < T::CA; ++i) {
-    const int r = (T::CA * wave + i) * 8 + r8;
+    const int r = (T::NW * i + wave) * 8 + r8;
     oa[i] = static_cast<uint32_t>((r < rows_a ? r : rows_a - 1) * g.Kp + 16 * unit);
   }
 #pragma unroll
   for (int i = 0; i < T::CW; ++i) {
-    const int r = (T::CW * wave + i) * 8 + r8;
+    const int r = (T::NW * i + wave) * 8 + r8;
     ow[i] = static_cast<uint32_t>((r < rows_w ? r : rows_w - 1) * g.Kp + 16 * unit);
   }
   const int rs = 64 * wave + lane;
   const uint32_t os = static_cast<uint32_t>((rs < rows_a ? rs : rows_a - 1) * C * 4);
 
-  auto copy = [&](int s, int c) {
+  // Copy `piece` of chunk c into stage s; a chunk past the end reads nothing (an
+  // empty buffer), so that the pipeline below needs no branch.
+  constexpr int kPieces = T::CA + T::CW;
+  const uint32_t bytes_a = static_cast<uint32_t>(rows_a * g.Kp);
+  const uint32_t bytes_w = static_cast<uint32_t>(rows_w * g.Kp);
+  auto copy = [&](int s, int c, int piece) {
     const uint32_t at = static_cast<uint32_t>(c) * kChunk;
-#pragma unroll
-    for (int i = 0; i < T::CA; ++i)
-      buffer_to_lds16(ba, &st[s].a[(T::CA * wave + i) * 8][0], oa[i], at);
-#pragma unroll
-    for (int i = 0; i < T::CW; ++i)
-      buffer_to_lds16(bw, &st[s].w[(T::CW * wave + i) * 8][0], ow[i], at);
-    // every fourth chunk: the scales of it and the next three
-    if (((c - c0) & 3) == 0 && wave < T::BM / 64)
+    if (piece < T::CA) {
+      buffer_to_lds16(make_buffer(g.a + m0 * g.Kp, c < c1 ? bytes_a : 0),
+                      &st[s].a[(T::NW * piece + wave) * 8][0], oa[piece < T::CA ? piece : 0], at);
+    } else if (piece < kPieces) {
+      const int i = piece - T::CA;
+      if ((i + 1) * T::NW * 8 <= T::BN || (T::NW * i + wave) * 8 < T::BN)
+        buffer_to_lds16(make_buffer(g.w + n0 * g.Kp, c < c1 ? bytes_w : 0),
+                        &st[s].w[(T::NW * i + wave) * 8][0], ow[i], at);
+    }
+  };
+  // The activation scales of chunk c and the next three, if c is the first of four.
+  auto copy_scales = [&](int c) {
+    if (c < c1 && ((c - c0) & 3) == 0 && wave < T::BM / 64)
       buffer_to_lds16(bs, &sal[((c - c0) >> 2) & 1][64 * wave][0], os, static_cast<uint32_t>(c) * 4);
   };
 
-  // the wave's weight scales, 64 groups at a time, one per lane
-  const int64_t nb_last = (g.N - 1) / kFp8Block;
-  const int64_t nb = (n0 + wn * NBN * 16) / kFp8Block;
-  const float* swp = g.sw + (nb < nb_last ? nb : nb_last) * C;
-  float swv = 0.f;
+  // The wave's columns lie in one or two blocks of weight scales; the scales of
+  // 64 groups at a time, one per lane.
+  static_assert(NBN * 16 <= kFp8Block, "two blocks of weight scales at most");
+  const int64_t nw0 = n0 + wn * NBN * 16, nb_last = (g.N - 1) / kFp8Block;
+  const int64_t nb0 = nw0 / kFp8Block < nb_last ? nw0 / kFp8Block : nb_last;
+  const int64_t nb1 = nb0 < nb_last ? nb0 + 1 : nb_last;
+  const int split_j = static_cast<int>(((nb0 + 1) * kFp8Block - nw0) / 16);   // first of block 1
+  float swv0 = 0.f, swv1 = 0.f;
+  auto load_sw = [&](int c) {
+    const bool in = c + lane < c1;
+    swv0 = in ? g.sw[nb0 * C + c + lane] : 0.f;
+    swv1 = in ? g.sw[nb1 * C + c + lane] : 0.f;
+  };
+  auto sw_of = [&](float v, int c) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), (c - c0) & 63));
+  };
 
   v4f acc[NBM][NBN];
 #pragma unroll
@@ -244,117 +282,157 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
 #pragma unroll
     for (int j = 0; j < NBN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  const int u0 = ((2 * q) ^ (lane & 7)) * 16, u1 = u0 ^ 16;
+  // A lane's 32 codes of a row are units q and q + 4 (the same K values on both
+  // sides, which is all that matters). A 16-byte LDS read serves lanes 0-3,
+  // 12-15 and 20-27 at once, then 4-11, 16-19 and 28-31: all 16 rows, with q
+  // differing by 1 between two sets of 8, which lands them on different units.
+  const int u0 = (q ^ (rl >> 1)) * 16, u1 = u0 ^ 64;
   auto frag = [&](const uint8_t (*rows)[kChunk], int block) {
     const uint8_t* p = rows[16 * block + rl];
     Frag<EXACT> f;
     f.set(*reinterpret_cast<const v4i*>(p + u0), *reinterpret_cast<const v4i*>(p + u1));
     return f;
   };
-
-  // Software pipeline. While row block i's products go out, the products of
-  // the block before it are added (two sets of partials), and block i+1 is read
-  // (two sets of activation operands); each matrix instruction is followed by
-  // the four additions of one issued NBN instructions earlier. The last block of
-  // a chunk needs nothing more from its stage, so the barrier stands before it:
-  // behind it go the copies of chunk c+2 into the stage just read, and the first
-  // operands of chunk c+1, which the copies of the chunk before have brought.
-  static_assert(NBM % 2 == 0, "the operand sets alternate across chunks too");
-  Frag<EXACT> fw[NBN], fa[2];
-  v4f p[2][NBN];
-  float raw[2] = {0.f, 0.f}, sw = 0.f, sw_prev = 0.f;
-#pragma unroll
-  for (int j = 0; j < NBN; ++j) p[1][j] = v4f{0.f, 0.f, 0.f, 0.f};
   auto scale_of = [&](int i, int c) {
     return sal[((c - c0) >> 2) & 1][(wm * NBM + i) * 16 + rl][(c - c0) & 3];
   };
-  auto wait_all = [&]() {              // this wave's copies and LDS reads, then every wave's
-    __builtin_amdgcn_s_waitcnt(kWaitAll);
+  // this wave's copies but the newest n and all its LDS reads, then every wave's
+  auto wait_but = [&](auto n) {
+    __builtin_amdgcn_s_waitcnt(wait_copies(decltype(n)::value));
     __builtin_amdgcn_s_barrier();
   };
-  swv = c0 + lane < c1 ? swp[c0 + lane] : 0.f;
-  copy(0, c0);
-  if (c0 + 1 < c1) copy(1, c0 + 1);
-  wait_all();
-  fa[0] = frag(st[0].a, wm * NBM);
-  float next_raw = scale_of(0, c0);
+
+  // Software pipeline. The wave holds its activation blocks of a chunk and
+  // streams its weight blocks, read D blocks ahead (the LDS answers later than
+  // the NBM instructions of one block take). Product n = NBM * j + i goes out
+  // with the four additions of product n - LAG behind it. A chunk's last D
+  // blocks are read before the barrier in front of block NBN - D, so behind it
+  // the stage is free: the copies of chunk c+NST go there, one every SP products
+  // and on into chunk c+1 (issued together they hold up every wave at once),
+  // and the blocks read ahead come from chunk c+1, whose copies the wait in
+  // front of the barrier is for.
+  constexpr int D = 2, LAG = NBM < 3 ? NBM : 3, TOT = NBM * NBN;
+  constexpr int SP = kPieces * 2 - D * NBM <= (NBN - D) * NBM ? 2 : 1;
+  constexpr int kEarly = (D * NBM + SP - 1) / SP;   // copies before the next chunk begins
+  constexpr int kUniform = T::CA + T::BN / 8 / T::NW;   // copies per chunk of every wave
+  static_assert(NBN % 2 == 0 && TOT % 4 == 0, "the four sets alternate across two chunks");
+  static_assert(NST == 2 || NST == 4, "stages and operand sets are fixed in a run of NST chunks");
+  static_assert(kPieces * SP - D * NBM <= (NBN - D) * NBM, "a chunk's copies precede its barrier");
+  Frag<EXACT> fa[NBM], fw[4];
+  v4f p[4];
+  float sa[NBM], pend[NBM];            // activation scales; scales of products not yet added
+  float sa_last[NBM], sw_last0 = 0.f, sw_last1 = 0.f;   // those of the chunk before
 #pragma unroll
-  for (int j = 0; j < NBN; ++j) fw[j] = frag(st[0].w, wn * NBN + j);
-  for (int c = c0; c < c1; ++c) {
-    const int s = (c - c0) & 1;
-    sw_prev = sw;
-    sw = __builtin_bit_cast(
-        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, swv), (c - c0) & 63));
+  for (int i = 0; i < NBM; ++i) sa[i] = sa_last[i] = pend[i] = 0.f;
 #pragma unroll
-    for (int i = 0; i < NBM; ++i) {
-      raw[i & 1] = next_raw;
-      if (i + 1 < NBM) {
-        fa[(i + 1) & 1] = frag(st[s].a, wm * NBM + i + 1);
-        next_raw = scale_of(i + 1, c);
-      } else {
-        if (((c - c0) & 63) == 63) swv = c + 1 + lane < c1 ? swp[c + 1 + lane] : 0.f;
-        wait_all();
-        if (c + 2 < c1) copy(s, c + 2);
-        fa[0] = frag(st[s ^ 1].a, wm * NBM);
-        next_raw = scale_of(0, c + 1);
+  for (int i = 0; i < 4; ++i) p[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  // acc += product set b, scaled, of row block i and weight block d
+  auto add = [&](int i, int d, int b, float scale) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][d][e] = __builtin_fmaf(p[b][e], scale, acc[i][d][e]);
+    // the sums are made here: without this the compiler moves them past the
+    // branches below and keeps every product of the chunk until then
+    asm volatile("" : "+v"(acc[i][d]));
+  };
+  // chunk c in stage S, its first weight block in operand set P
+  auto chunk = [&](int c, auto stage, auto first) {
+    constexpr int S = decltype(stage)::value, P = decltype(first)::value;
+    const float sw0 = sw_of(swv0, c), sw1 = sw_of(swv1, c);
+#pragma unroll
+    for (int j = 0; j < NBN; ++j) {
+      if (j == NBN - D) {
+        if (S == NST - 1 && ((c - c0) & 63) == 63) {
+          load_sw(c + 1);
+          __builtin_amdgcn_s_waitcnt(wait_vmem(0));
+        }
+        wait_but(std::integral_constant<int, (NST - 2) * kUniform>{});
+        copy_scales(c + NST);
       }
-      // the scale of the products added here: row block i-1 of this chunk, or
-      // the last block of the chunk before
-      const float scale = raw[(i + 1) & 1] * (i > 0 ? sw : sw_prev);
+      fw[(P + j + D) & 3] = j + D < NBN ? frag(st[S].w, wn * NBN + j + D)
+                                        : frag(st[(S + 1) % NST].w, wn * NBN + j + D - NBN);
+      float scale[NBM];
+#pragma unroll
+      for (int i = 0; i < NBM; ++i) scale[i] = sa[i] * (j < split_j ? sw0 : sw1);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < NBN; ++j) {
-        p[i & 1][j] = mfma_group(fw[j], fa[i & 1]);
-        if (i + 1 == NBM) fw[j] = frag(st[s ^ 1].w, wn * NBN + j);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int d = (i + NBM - 1) % NBM;
-          acc[d][j][e] = __builtin_fmaf(p[(i + 1) & 1][j][e], scale, acc[d][j][e]);
+      for (int i = 0; i < NBM; ++i) {
+        const int n = j * NBM + i;
+        p[n & 3] = mfma_group(fw[(P + j) & 3], fa[i]);
+        const int behind = n - (NBN - D) * NBM, cont = n + D * NBM;
+        if (behind >= 0 && behind % SP == 0) copy(S, c + NST, behind / SP);
+        if (cont < kPieces * SP && cont % SP == 0)
+          copy((S + NST - 1) % NST, c + NST - 1, cont / SP);
+        if (j + 1 == NBN) fa[i] = frag(st[(S + 1) % NST].a, wm * NBM + i);
+        const int m = (n + TOT - LAG) % TOT, mi = m % NBM, mj = m / NBM;
+        add(mi, mj, (n - LAG) & 3,
+            n >= LAG ? pend[mi] : sa_last[mi] * (mj < split_j ? sw_last0 : sw_last1));
+        pend[i] = scale[i];
+        if (j + 1 == NBN) {
+          sa_last[i] = sa[i];
+          sa[i] = scale_of(i, c + 1);
         }
-        // the sums are made here: without this the compiler moves them past the
-        // branches below and keeps every partial of the chunk until then
-        asm volatile("" : "+v"(acc[(i + NBM - 1) % NBM][j]));
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-  }
-  {
-    const float scale = raw[1] * sw;
+    sw_last0 = sw0;
+    sw_last1 = sw1;
+  };
+  load_sw(c0);
+  __builtin_amdgcn_s_waitcnt(wait_vmem(0));
 #pragma unroll
-    for (int j = 0; j < NBN; ++j)
+  for (int t = 0; t < NST; ++t) {
+    copy_scales(c0 + t);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        acc[NBM - 1][j][e] = __builtin_fmaf(p[1][j][e], scale, acc[NBM - 1][j][e]);
+    for (int k = 0; k < (t + 1 < NST ? kPieces : kEarly); ++k) copy(t, c0 + t, k);
   }
+  wait_but(std::integral_constant<int, (NST - 2) * kUniform>{});
+#pragma unroll
+  for (int j = 0; j < D; ++j) fw[j] = frag(st[0].w, wn * NBN + j);
+#pragma unroll
+  for (int i = 0; i < NBM; ++i) {
+    fa[i] = frag(st[0].a, wm * NBM + i);
+    sa[i] = scale_of(i, c0);
+  }
+  for (int c = c0; c < c1; c += NST) {
+    static_for<NST>([&](auto t) {
+      constexpr int S = decltype(t)::value;
+      if (S == 0 || c + S < c1)
+        chunk(c + S, t, std::integral_constant<int, (S * NBN) & 3>{});
+    });
+  }
+#pragma unroll
+  for (int m = TOT - LAG; m < TOT; ++m) {
+    const int mi = m % NBM, mj = m / NBM;
+    add(mi, mj, m & 3, sa_last[mi] * (mj < split_j ? sw_last0 : sw_last1));
+  }
+  wait_but(std::integral_constant<int, 0>{});   // the stages are free
 
-  const int64_t mw = m0 + wm * NBM * 16 + rl, nw = n0 + wn * NBN * 16 + 4 * q;
-  // A 16-bit Y goes out through the wave's share of the stages, where a row's
-  // 64 columns make one 128-byte line: 8 lanes store a whole line, instead of 4
-  // lanes a 32-byte piece of it.
-  if constexpr (YT != SVDQ_F32 && NBN == 4) {
-    static_assert(sizeof(st) >= static_cast<size_t>(T::NW) * NBM * 16 * 128, "room for the tile");
-    __syncthreads();                   // the last operands read ahead are not needed
-    const int64_t n_wave = n0 + wn * 64;
-    if (g.slices == 1 && n_wave + 64 <= g.N &&
+  const int64_t mw = m0 + wm * NBM * 16, nw = nw0 + 4 * q;
+  // A 16-bit Y goes out through the wave's share of LDS, from where a
+  // lane stores 16 bytes and its neighbours the rest of the row's columns,
+  // instead of 4 lanes a 32-byte piece of it. Rows of 32 * NBN bytes, padded by
+  // 16 to spread the banks.
+  if constexpr (YT != SVDQ_F32) {
+    constexpr int RB = 32 * NBN + 16, UN = 2 * NBN;   // bytes and 16-byte units of a row
+    static_assert(sizeof(lds) >= static_cast<size_t>(T::NW) * NBM * 16 * RB, "room for the tile");
+    if (g.slices == 1 && nw0 + NBN * 16 <= g.N &&
         ((reinterpret_cast<uintptr_t>(g.Y) | (g.ldy * 2)) & 15) == 0) {
-      uint8_t* mem = reinterpret_cast<uint8_t*>(&st) + wave * NBM * 16 * 128;
+      uint8_t* mem = reinterpret_cast<uint8_t*>(&lds) + wave * NBM * 16 * RB;
 #pragma unroll
       for (int j = 0; j < NBN; ++j) {
         const v4f b = bias4(g, nw + 16 * j);
 #pragma unroll
-        for (int i = 0; i < NBM; ++i) {
-          const int row = 16 * i + rl, u = (2 * j + (q >> 1)) ^ (row & 7);
-          *reinterpret_cast<uint2*>(mem + row * 128 + u * 16 + (q & 1) * 8) =
+        for (int i = 0; i < NBM; ++i)
+          *reinterpret_cast<uint2*>(mem + (16 * i + rl) * RB + 32 * j + 8 * q) =
               round4<YT, GELU>(acc[i][j], b);
-        }
       }
-      const int64_t m_wave = m0 + wm * NBM * 16;
-      uint16_t* y = static_cast<uint16_t*>(g.Y) + n_wave + 8 * (lane & 7);
+      uint16_t* y = static_cast<uint16_t*>(g.Y) + mw * g.ldy + nw0;
+      const int rows = static_cast<int>(g.M - mw < NBM * 16 ? g.M - mw : NBM * 16);
 #pragma unroll
-      for (int t = 0; t < 2 * NBM; ++t) {
-        const int row = 8 * t + r8;
-        const v4i v = *reinterpret_cast<const v4i*>(mem + row * 128 + (((lane & 7) ^ r8) << 4));
-        if (m_wave + row < g.M) *reinterpret_cast<v4i*>(y + (m_wave + row) * g.ldy) = v;
+      for (int t = 0; t < NBM * 16 * UN / 64; ++t) {
+        const int at = 64 * t + lane, row = at / UN, col = at % UN;
+        const v4i v = *reinterpret_cast<const v4i*>(mem + row * RB + 16 * col);
+        if (row < rows) *reinterpret_cast<v4i*>(y + row * g.ldy + 8 * col) = v;
       }
       return;
     }
@@ -364,18 +442,20 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
     for (int j = 0; j < NBN; ++j) {
       const v4f b = bias4(g, nw + 16 * j);
 #pragma unroll
-      for (int i = 0; i < NBM; ++i) finish4<YT, GELU>(g, acc[i][j], b, mw + 16 * i, nw + 16 * j);
+      for (int i = 0; i < NBM; ++i)
+        finish4<YT, GELU>(g, acc[i][j], b, mw + 16 * i + rl, nw + 16 * j);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NBM; ++i) {
-      if (mw + 16 * i >= g.M) continue;
-      float* p = g.part + (slice * g.M + mw + 16 * i) * g.N;
+      const int64_t m = mw + 16 * i + rl;
+      if (m >= g.M) continue;
+      float* out = g.part + (slice * g.M + m) * g.N;
 #pragma unroll
       for (int j = 0; j < NBN; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (nw + 16 * j + e < g.N) p[nw + 16 * j + e] = acc[i][j][e];
+          if (nw + 16 * j + e < g.N) out[nw + 16 * j + e] = acc[i][j][e];
     }
   }
 }
@@ -402,9 +482,10 @@ __global__ __launch_bounds__(256) void gemm_fp8_join(const GemmArgs g) {
 
 constexpr int kRowWaves = 8;
 
-template <int NBM, int YT, bool GELU>
+template <int YT, bool GELU>
 __global__ __launch_bounds__(64 * kRowWaves) void gemm_fp8_rows(const GemmArgs g) {
   constexpr bool EXACT = YT == SVDQ_F32;
+  constexpr int NBM = 1;
   __shared__ v4f sums[kRowWaves][NBM][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
@@ -425,7 +506,6 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_fp8_rows(const GemmArgs g
   v4f acc[NBM];
 #pragma unroll
   for (int i = 0; i < NBM; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
   for (int c = wave; c < C; c += kRowWaves) {
     const int64_t at = static_cast<int64_t>(c) * kChunk;
     const v4i* wp = reinterpret_cast<const v4i*>(w + at);
@@ -457,32 +537,73 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_fp8_rows(const GemmArgs g
   }
 }
 
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 16;
 
-int split_slices(int64_t M, int64_t N, int64_t Kp) {
-  if (M <= kFewRows) return 1;
-  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64);
-  const int64_t C = Kp / kChunk;
-  int64_t s = resident_slots() / tiles;
-  if (s > C / 8) s = C / 8;
-  return s < 2 ? 1 : static_cast<int>(s < 16 ? s : 16);
+// The tile kernels' variants and their measured cost in microseconds: of a
+// chunk when a workgroup has the chip almost to itself and when every slot is
+// taken, and of a tile's start and end.
+struct TileCost {
+  int bm, bn, per_cu;
+  float alone, full, ends;
+};
+constexpr TileCost kTiles16[] = {{256, 256, 1, 1.25f, 1.55f, 7.0f},
+                                 {256, 192, 1, 1.06f, 1.35f, 6.0f},
+                                 {128, 128, 2, 0.77f, 1.00f, 4.0f},
+                                 {64, 128, 3, 0.60f, 0.95f, 4.0f},
+                                 {64, 64, 2, 0.24f, 0.40f, 2.5f}};
+constexpr TileCost kTiles32[] = {{256, 128, 1, 1.60f, 2.10f, 6.0f},
+                                 {64, 128, 3, 0.90f, 1.65f, 4.0f},
+                                 {64, 64, 2, 0.50f, 0.72f, 2.5f}};
+
+struct GemmPlan {
+  int tile, slices;
+};
+
+// The variant and the split along K of least estimated time. A round of tiles
+// that leaves slots empty runs its chunks the faster. A split costs a second
+// launch and the partial tiles written and read, about 7 us and 2.5 TB/s.
+// Against the best of all variants on 24 shapes from 65 x 3072 x 3072 to
+// 4608 x 12288 x 3072 the choice is within 4% on 22 and 12% on the others.
+template <int COUNT>
+GemmPlan least(const TileCost (&tiles)[COUNT], int64_t M, int64_t N, int64_t Kp, bool split) {
+  const int64_t C = Kp / kChunk, cus = resident_slots() / 2;
+  GemmPlan best{0, 1};
+  float least = -1.f;
+  for (int t = 0; t < COUNT; ++t) {
+    const TileCost& k = tiles[t];
+    for (int s = 1; s <= (split ? 16 : 1) && s * 2 <= C + 1; s *= 2) {
+      const int64_t wgs = ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn) * s;
+      const int64_t slots = cus * k.per_cu, rounds = wgs / slots;
+      const float chunks = static_cast<float>((C + s - 1) / s);
+      const float part = static_cast<float>(wgs - rounds * slots) / static_cast<float>(slots);
+      float us = static_cast<float>(rounds) * (chunks * k.full + k.ends);
+      if (part > 0.f) us += chunks * (k.alone + part * (k.full - k.alone)) + k.ends;
+      if (s > 1) us += 7.f + static_cast<float>(M) * static_cast<float>(N) * s * 8.f / 2.5e6f;
+      if (least < 0.f || us < least) {
+        least = us;
+        best = GemmPlan{t, s};
+      }
+    }
+  }
+  return best;
+}
+
+GemmPlan gemm_plan(int64_t M, int64_t N, int64_t Kp, bool f32, bool split) {
+  return f32 ? least(kTiles32, M, N, Kp, split) : least(kTiles16, M, N, Kp, split);
 }
 
 template <int YT, bool GELU>
 void launch_rows(const GemmArgs& g, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((g.N + 15) / 16)), block(64 * kRowWaves);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, g); };
-  if (g.M <= 16) go(gemm_fp8_rows<1, YT, GELU>);
-  else if (g.M <= 32) go(gemm_fp8_rows<2, YT, GELU>);
-  else go(gemm_fp8_rows<4, YT, GELU>);
+  hipLaunchKernelGGL((gemm_fp8_rows<YT, GELU>), dim3(static_cast<unsigned>((g.N + 15) / 16)),
+                     dim3(64 * kRowWaves), 0, stream, g);
 }
 
-template <int WM, int WN, int NBM, int NBN, int YT, bool GELU>
+template <int WM, int WN, int NBM, int NBN, int NST, int YT, bool GELU>
 void launch_tiles(const GemmArgs& g, hipStream_t stream) {
-  using T = Tile<WM, WN, NBM, NBN>;
+  using T = Tile<WM, WN, NBM, NBN, NST>;
   const int tiles_m = static_cast<int>((g.M + T::BM - 1) / T::BM);
   const int tiles_n = static_cast<int>((g.N + T::BN - 1) / T::BN);
-  hipLaunchKernelGGL((gemm_fp8_tiles<WM, WN, NBM, NBN, YT, GELU>),
+  hipLaunchKernelGGL((gemm_fp8_tiles<WM, WN, NBM, NBN, NST, YT, GELU>),
                      dim3(static_cast<unsigned>(tiles_m * tiles_n * g.slices)), dim3(64 * T::NW),
                      0, stream, g, tiles_m, tiles_n);
 }
@@ -493,29 +614,36 @@ hipError_t launch_e(GemmArgs& g, hipStream_t stream) {
     launch_rows<YT, GELU>(g, stream);
     return hipGetLastError();
   }
-  const int64_t big = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-  if (big >= resident_slots() / 4) {
-    g.slices = 1;
-    // an fp32 output's operands take twice the registers
-    launch_tiles<2, 4, YT == SVDQ_F32 ? 4 : 8, 4, YT, GELU>(g, stream);
-    return hipGetLastError();
+  const GemmPlan p = gemm_plan(g.M, g.N, g.Kp, YT == SVDQ_F32, g.part != nullptr);
+  g.slices = p.slices;
+  if constexpr (YT == SVDQ_F32) {
+    // operands widened to fp16 take twice the registers
+    if (p.tile == 0) launch_tiles<4, 2, 4, 4, 2, YT, GELU>(g, stream);
+    else if (p.tile == 1) launch_tiles<2, 2, 2, 4, 2, YT, GELU>(g, stream);
+    else launch_tiles<2, 2, 2, 2, 4, YT, GELU>(g, stream);
+  } else {
+    if (p.tile == 0) launch_tiles<4, 2, 4, 8, 2, YT, GELU>(g, stream);
+    else if (p.tile == 1) launch_tiles<4, 2, 4, 6, 2, YT, GELU>(g, stream);
+    else if (p.tile == 2) launch_tiles<2, 2, 4, 4, 2, YT, GELU>(g, stream);
+    else if (p.tile == 3) launch_tiles<2, 2, 2, 4, 2, YT, GELU>(g, stream);
+    else launch_tiles<2, 2, 2, 2, 4, YT, GELU>(g, stream);
   }
-  g.slices = g.part != nullptr ? split_slices(g.M, g.N, g.Kp) : 1;
-  launch_tiles<2, 2, 2, 2, YT, GELU>(g, stream);
-  if (g.slices > 1) {
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int64_t threads = g.M * ((g.N + 3) / 4);
-    hipLaunchKernelGGL((gemm_fp8_join<YT, GELU>), dim3(static_cast<unsigned>((threads + 255) / 256)),
-                       dim3(256), 0, stream, g);
-  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || g.slices == 1) return e;
+  const int64_t threads = g.M * ((g.N + 3) / 4);
+  hipLaunchKernelGGL((gemm_fp8_join<YT, GELU>), dim3(static_cast<unsigned>((threads + 255) / 256)),
+                     dim3(256), 0, stream, g);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Enough for either precision's plan: the output's type is not known here.
 size_t gemm_fp8_split_bytes(int64_t M, int64_t N, int64_t Kp) {
-  const int s = split_slices(M, N, Kp);
+  if (M <= kFewRows) return 0;
+  const int s16 = gemm_plan(M, N, Kp, false, true).slices;
+  const int s32 = gemm_plan(M, N, Kp, true, true).slices;
+  const int s = s16 > s32 ? s16 : s32;
   return s > 1 ? static_cast<size_t>(s) * M * N * 4 : 0;
 }
 
