@@ -304,8 +304,9 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
                                                      attention_ml_bytes(B, Lq, Hq, p.splits))
                           : nullptr;
   constexpr float kLog2e = 1.4426950408889634f;
-  g.scale2 = scale * kLog2e;
-  g.cap_in = softcap > 0.f ? 2.0f * kLog2e * (scale / softcap) : 0.f;
+  g.q_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
+  g.scale2 = g.q_sign != 0 ? std::fabs(scale) * kLog2e : 1.f;
+  g.cap_in = softcap > 0.f ? 2.0f * kLog2e * (std::fabs(scale) / softcap) : 0.f;
   g.cap2 = softcap * kLog2e;
   g.B = static_cast<int>(B);
   g.Lq = static_cast<int>(Lq);

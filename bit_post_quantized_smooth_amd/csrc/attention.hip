@@ -45,6 +45,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kWaves = 4;
+constexpr float kGrow = 8.f;
+constexpr float kLarge = 1e6f;       // logits (base 2); their rounding is below 2^-4
 
 template <class T>
 struct Half;
@@ -54,8 +56,7 @@ struct Half<_Float16> {
   static __device__ __forceinline__ v16f mfma(v8h a, v8h b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
-  static constexpr uint32_t kExp = 0x7C007C00u;     // exponent bits of two values
-  static constexpr uint16_t kOne = 0x3C00, kExp1 = 0x7C00, kFrac = 0x03FF;
+  static constexpr uint16_t kOne = 0x3C00, kInf = 0x7C00;
 };
 template <>
 struct Half<__bf16> {
@@ -63,12 +64,12 @@ struct Half<__bf16> {
   static __device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  static constexpr uint32_t kExp = 0x7F807F80u;
-  static constexpr uint16_t kOne = 0x3F80, kExp1 = 0x7F80, kFrac = 0x007F;
+  static constexpr uint16_t kOne = 0x3F80, kInf = 0x7F80;
 };
 
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
+typedef unsigned short v8u __attribute__((ext_vector_type(8)));
 
 // max over the two lanes that share a row (lane and lane ^ 32); sum likewise
 __device__ __forceinline__ void half_pair(float x, float& a, float& b) {
@@ -87,6 +88,13 @@ __device__ __forceinline__ float half_sum(float x) {
   float a, b;
   half_pair(x, a, b);
   return a + b;
+}
+
+// A transposing read: 16 lanes bring 4 rows x 16 channels, lane i gets channel i
+// of the 4 rows. The restrict pointer is there for the compiler's alias
+// information: without any, it makes the read wait for every copy in flight.
+__device__ __forceinline__ v4s read_tr(const uint8_t* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p));
 }
 
 // RW waves along the rows, 4 / RW along the keys of a tile.
@@ -119,28 +127,36 @@ struct Attention {
   int hk;
   vec qf[DS];
   v16f o[DB];
-  float m, l;                                       // row maximum (base 2), this half's sum
-  int lo, hi, pos;                                  // the row's keys, its own position
+  // the row's reference maximum (base 2) and this half's sum. The reference only
+  // follows the running maximum when that has grown by more than kGrow: until
+  // then exp2(x - m) stays below 2^kGrow and nothing needs rescaling.
+  float m, l;
+  int lo, pos;                                      // the row's first key, its own position
+  uint32_t width;                                   // keys it sees, from lo on
+  bool large;                                       // a reference beyond kLarge
   int w_lo, w_hi, w_lo_max, w_hi_min;               // over the wave's rows
   float slope2;
   uint32_t koff[CPW], voff[CPW];
 
   __device__ __forceinline__ Attention(const AttnArgs& args, Lds& shared) : g(args), lds(shared) {}
 
-  __device__ __forceinline__ void copy(int s, int key0, int keys) {
-    const char* kb = static_cast<const char*>(g.k) + (b * g.k_b + hk * g.k_h + key0 * g.k_l) * 2;
-    const char* vb = static_cast<const char*>(g.v) + (b * g.v_b + hk * g.v_h + key0 * g.v_l) * 2;
+  __device__ __forceinline__ void copy_k(int s, int key0, int keys) {
+    const char* base = static_cast<const char*>(g.k) + (b * g.k_b + hk * g.k_h + key0 * g.k_l) * 2;
     const int n = keys < KT ? keys : KT;
-    const __amdgpu_buffer_rsrc_t bk =
-        make_buffer(kb, static_cast<uint32_t>(((n - 1) * g.k_l + g.D) * 2));
-    const __amdgpu_buffer_rsrc_t bv =
-        make_buffer(vb, static_cast<uint32_t>(((n - 1) * g.v_l + g.D) * 2));
+    const __amdgpu_buffer_rsrc_t buf =
+        make_buffer(base, static_cast<uint32_t>(((n - 1) * g.k_l + g.D) * 2));
 #pragma unroll
     for (int i = 0; i < CPW; ++i)
-      buffer_to_lds16(bk, &lds.k[s][(CPW * wave + i) * RPC][0], koff[i], 0);
+      buffer_to_lds16(buf, &lds.k[s][(CPW * wave + i) * RPC][0], koff[i], 0);
+  }
+  __device__ __forceinline__ void copy_v(int s, int key0, int keys) {
+    const char* base = static_cast<const char*>(g.v) + (b * g.v_b + hk * g.v_h + key0 * g.v_l) * 2;
+    const int n = keys < KT ? keys : KT;
+    const __amdgpu_buffer_rsrc_t buf =
+        make_buffer(base, static_cast<uint32_t>(((n - 1) * g.v_l + g.D) * 2));
 #pragma unroll
     for (int i = 0; i < CPW; ++i)
-      buffer_to_lds16(bv, &lds.v[s][(CPW * wave + i) * RPC][0], voff[i], 0);
+      buffer_to_lds16(buf, &lds.v[s][(CPW * wave + i) * RPC][0], voff[i], 0);
   }
 
   // Unit u of row r lies at u ^ twist(r). LDS has 64 banks of 4 bytes. A read of
@@ -163,128 +179,203 @@ struct Attention {
       const int row = key + 8 * e + 4 * (g16 >> 1) + (a >> 2);
       const int unit = (ch >> 3) ^ twist(row);
       const uint8_t* p = &lds.v[s][row][unit * 16 + (ch & 4) * 2];
-      part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) v4s*)(p));
+      part[e] = read_tr(p);
     }
     return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
   }
 
-  // Scores of one 32-key block to base-2 logits; key0 is the key of row 0 of
-  // the block.
+  // Without a cap and slopes a score stays as the products give it and its scale
+  // goes into the exponential; with them it is made a base-2 logit here.
+  static constexpr bool RAW = !CAP && !SLOPES;
+
+  // x = K Q^T of the 32 keys from LDS row `row0` on, in stage s
+  __device__ __forceinline__ v16f products(int s, int row0) {
+    v16f x;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+    const int row = row0 + rl;
+#pragma unroll
+    for (int t = 0; t < DS; ++t) {
+      const int unit = (2 * t + h) ^ twist(row);
+      const v4i kf = *reinterpret_cast<const v4i*>(&lds.k[s][row][unit * 16]);
+      x = Half<T>::mfma(__builtin_bit_cast(vec, kf), qf[t], x);
+    }
+    return x;
+  }
+
+  // Scores to logits (see RAW) with the masked ones at -inf; the largest of this
+  // lane's in base 2. key0: the block's first key.
   template <bool MASK>
-  __device__ __forceinline__ void logits(v16f& s, int key0) {
+  __device__ __forceinline__ float logits(v16f& x, int key0) {
+    float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int key = key0 + (i & 3) + 8 * (i >> 2) + 4 * h;
-      float x = s[i];
+      float v = x[i];
       if constexpr (CAP) {
         // cap * tanh(y) with tanh(y) = 1 - 2 / (exp(2 y) + 1)
-        const float e = __builtin_amdgcn_exp2f(x * g.cap_in);
-        x = g.cap2 - 2.0f * g.cap2 * __builtin_amdgcn_rcpf(e + 1.0f);
-      } else {
-        x = x * g.scale2;
+        const float e = __builtin_amdgcn_exp2f(v * g.cap_in);
+        v = __builtin_fmaf(-2.0f * g.cap2, __builtin_amdgcn_rcpf(e + 1.0f), g.cap2);
+      } else if constexpr (SLOPES) {
+        v = v * g.scale2;
       }
-      if constexpr (SLOPES) x = __builtin_fmaf(-slope2, fabsf(static_cast<float>(pos - key)), x);
-      if constexpr (MASK) x = key >= lo && key < hi ? x : kNegInf;
-      s[i] = x;
+      if constexpr (SLOPES)
+        v = __builtin_fmaf(-slope2, fabsf(static_cast<float>(pos - key)), v);
+      if constexpr (MASK) v = static_cast<uint32_t>(key - lo) < width ? v : kNegInf;
+      x[i] = v;
+      top = fmaxf(top, v);
     }
+    return RAW ? top * g.scale2 : top;
   }
 
-  // O^T += V^T P^T for 16 keys of a block whose masks hide some of them. A
-  // hidden key has P = 0, but 0 times an infinity or a NaN in V would reach
-  // the rows that do not see it: such values are taken out of the operand, and
-  // their effect (an infinity of their sign, or NaN) is added to the rows that
-  // do see them, found as matrix products of indicators.
-  __device__ __forceinline__ void pv_masked(int s, int krow, int key0, const v8s& p) {
-    v8s sees;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int key = key0 + (e & 3) + 8 * (e >> 2) + 4 * h;
-      sees[e] = key >= lo && key < hi ? static_cast<short>(Half<T>::kOne) : short{0};
-    }
-#pragma unroll
-    for (int d = 0; d < DB; ++d) {
-      v8s v = v_frag(s, krow, d);
-      bool odd = false;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) odd |= (v[e] & Half<T>::kExp1) == Half<T>::kExp1;
-      if (__builtin_amdgcn_ballot_w64(odd) != 0) {
-        v8s up, down;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint16_t x = static_cast<uint16_t>(v[e]);
-          const bool bad = (x & Half<T>::kExp1) == Half<T>::kExp1;
-          const bool nan = bad && (x & Half<T>::kFrac) != 0;
-          up[e] = bad && (nan || !(x & 0x8000)) ? static_cast<short>(Half<T>::kOne) : short{0};
-          down[e] = bad && (nan || (x & 0x8000)) ? static_cast<short>(Half<T>::kOne) : short{0};
-          if (bad) v[e] = 0;
-        }
-        v16f zero;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) zero[i] = 0.f;
-        const v16f nu = Half<T>::mfma(__builtin_bit_cast(vec, up), __builtin_bit_cast(vec, sees), zero);
-        const v16f nd = Half<T>::mfma(__builtin_bit_cast(vec, down), __builtin_bit_cast(vec, sees), zero);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (nu[i] > 0.f) o[d][i] = o[d][i] - kNegInf;
-          if (nd[i] > 0.f) o[d][i] = o[d][i] + kNegInf;
-        }
-      }
-      o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v), __builtin_bit_cast(vec, p), o[d]);
-    }
+  // Whether a block's largest logits (the row's, of both halves) outgrow the
+  // reference in any row; the new reference if so.
+  __device__ __forceinline__ bool outgrows(float top) const {
+    return __builtin_amdgcn_ballot_w64(top > m + kGrow) != 0;
   }
-
-  // One tile, whose row 0 is key0, from stage s.
-  template <bool MASK>
-  __device__ __forceinline__ void tile(int s, int key0) {
-    v16f x[KB];
-    float top = kNegInf;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      const int krow = 32 * (KB * kw + kb);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[kb][i] = 0.f;
-      const int row = krow + rl;
-#pragma unroll
-      for (int t = 0; t < DS; ++t) {
-        const int unit = (2 * t + h) ^ twist(row);
-        const v4i kf = *reinterpret_cast<const v4i*>(&lds.k[s][row][unit * 16]);
-        x[kb] = Half<T>::mfma(__builtin_bit_cast(vec, kf), qf[t], x[kb]);
-      }
-      logits<MASK>(x[kb], key0 + krow);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, x[kb][i]);
-    }
-    const float m_new = fmaxf(m, half_max(top));
-    const float base = m_new == kNegInf ? 0.f : m_new;      // a row that has seen no key yet
-    const float alpha = __builtin_amdgcn_exp2f(m - base);
+  __device__ __forceinline__ void raise(float top) {
+    const float m_new = fmaxf(m, top);
+    const float alpha = m_new == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
     m = m_new;
+    large = __builtin_amdgcn_ballot_w64(m > kLarge || (m < -kLarge && m != kNegInf)) != 0;
     l = l * alpha;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][i] = o[d][i] * alpha;
+  }
+  // what the exponentials subtract; -inf: a row that has seen no key yet
+  __device__ __forceinline__ float base() const { return m == kNegInf ? 0.f : m; }
+
+  // x -> P in 16 bits (the operands of 16 keys each), and their sum. FUSED: scale
+  // * x - base in one rounding. That leaves a factor of the row, from the rounding
+  // of base, which the division by the sum takes out, unless base is so large
+  // that the factor overflows: then the product is rounded as base was.
+  template <bool FUSED>
+  __device__ __forceinline__ void exponentials(const v16f& x, vec (&p)[2]) {
+    const float sub = base();
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      const int krow = 32 * (KB * kw + kb);
-      vec p[2];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float e = __builtin_amdgcn_exp2f(x[kb][i] - base);
-        l = l + e;
-        p[i >> 3][i & 7] = static_cast<T>(e);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if constexpr (MASK) {
-          pv_masked(s, krow + 16 * t, key0 + krow + 16 * t, __builtin_bit_cast(v8s, p[t]));
-        } else {
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-            o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v_frag(s, krow + 16 * t, d)), p[t], o[d]);
-        }
-      }
+    for (int i = 0; i < 16; ++i) {
+      const float e = __builtin_amdgcn_exp2f(!RAW    ? x[i] - sub
+                                             : FUSED ? __builtin_fmaf(x[i], g.scale2, -sub)
+                                                     : x[i] * g.scale2 - sub);
+      l = l + e;
+      p[i >> 3][i & 7] = static_cast<T>(e);
     }
+  }
+
+  // O^T += V^T P^T over the 32 keys from row0 on in stage s, every key seen
+  __device__ __forceinline__ void pv(int s, int row0, const vec (&p)[2]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v_frag(s, row0 + 16 * t, d)), p[t], o[d]);
+  }
+
+  // The same where masks hide keys from some rows. A hidden key has P = 0, but 0
+  // times an infinity or a NaN in V would reach the rows that do not see it. So
+  // the operands are looked through first; where there is such a value it is
+  // taken out of the operand, and add_special() brings it to the rows that do see
+  // its key.
+  __device__ __forceinline__ void pv_masked(int s, int row0, int key0, const vec (&p)[2]) {
+    bool special = false;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      v8s v[DB];
+      v8u big = v8u{0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        v[d] = v_frag(s, row0 + 16 * t, d);
+        big = __builtin_elementwise_max(big, __builtin_bit_cast(v8u, v[d] & short{0x7FFF}));
+      }
+      uint16_t most = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = most > big[e] ? most : big[e];
+      if (__builtin_amdgcn_ballot_w64(most >= Half<T>::kInf) != 0) {
+        special = true;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((static_cast<uint16_t>(v[d][e]) & 0x7FFF) >= Half<T>::kInf) v[d][e] = 0;
+      }
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v[d]), p[t], o[d]);
+    }
+    if (special) add_special(s, row0, key0);
+  }
+
+  // o += every infinity and NaN of V in the block's keys that the row sees (as
+  // often as each is looked at; the sum is the same).
+  __device__ __forceinline__ void add_special(int s, int row0, int key0) {
+#pragma unroll 1
+    for (int k = 0; k < 32; ++k) {
+      const bool seen = static_cast<uint32_t>(key0 + k - lo) < width;
+      const uint8_t* row = &lds.v[s][row0 + k][0];
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int ch = 32 * d + 8 * e + 4 * h, unit = (ch >> 3) ^ twist(row0 + k);
+          typedef T vec4 __attribute__((ext_vector_type(4)));
+          const v4s bits = *reinterpret_cast<const v4s*>(row + unit * 16 + (ch & 4) * 2);
+          const vec4 val = __builtin_bit_cast(vec4, bits);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const bool take = seen && (static_cast<uint16_t>(bits[c]) & 0x7FFF) >= Half<T>::kInf;
+            o[d][4 * e + c] = o[d][4 * e + c] + (take ? static_cast<float>(val[c]) : 0.f);
+          }
+        }
+    }
+  }
+
+  // One block of 32 keys, whose first row in stage s is row0 and first key key0,
+  // masked, with logits of any size.
+  __device__ __forceinline__ void block(int s, int row0, int key0) {
+    v16f x = products(s, row0);
+    const float top = half_max(logits<true>(x, key0));
+    if (outgrows(top)) raise(top);
+    vec p[2];
+    exponentials<false>(x, p);
+    pv_masked(s, row0, key0, p);
+  }
+
+  // The wave's two blocks of a tile that every row sees whole: the softmax of one
+  // block runs on the vector unit beside the products of the other on the matrix
+  // cores. A block that outgrows the reference, and logits too large for the
+  // fused exponential, are left to block(). Returns the blocks done.
+  __device__ __forceinline__ int pair(int s, int row0, int key0) {
+    v16f x = products(s, row0);
+    vec p[2], r[2];
+    if (outgrows(half_max(logits<false>(x, key0))) || (RAW && large)) return 0;
+    __builtin_amdgcn_sched_barrier(0);
+    v16f y = products(s, row0 + 32);
+    exponentials<true>(x, p);
+#pragma unroll
+    for (int i = 0; i < DS; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 56 / DS, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (outgrows(half_max(logits<false>(y, key0 + 32)))) {
+      pv(s, row0, p);
+      return 1;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    pv(s, row0, p);
+    exponentials<true>(y, r);
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 28 / DB, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    pv(s, row0 + 32, r);
+    return 2;
   }
 
   __device__ __forceinline__ void run() {
@@ -309,7 +400,7 @@ struct Attention {
     pos = i + g.Lk - g.Lq;
     slope2 = SLOPES ? g.slopes[head] * kLog2e : 0.f;
     lo = 0;
-    hi = g.Lk;
+    int hi = g.Lk;
     if (g.ranges != nullptr) {
       const int32_t* p = g.ranges + b * g.range_b + 2 * static_cast<int64_t>(i);
       lo = p[0] > 0 ? p[0] : 0;
@@ -320,7 +411,8 @@ struct Attention {
       const int c = pos + 1 > pre ? pos + 1 : pre;
       hi = c < hi ? c : hi;
     }
-    if (!real || hi <= lo) {          // sees nothing
+    width = real && hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
+    if (width == 0) {                 // sees nothing
       lo = g.Lk;
       hi = 0;
     }
@@ -366,7 +458,11 @@ struct Attention {
       koff[c] = in ? static_cast<uint32_t>((row * g.k_l + unit * 8) * 2) : 0xFFFFFFF0u;
       voff[c] = in ? static_cast<uint32_t>((row * g.v_l + unit * 8) * 2) : 0xFFFFFFF0u;
     }
-    if (t0 < t1) copy(0, first + t0 * KT, last - (first + t0 * KT));
+    const int start = first + t0 * KT;
+    if (t0 < t1) {
+      copy_k(0, start, last - start);
+      copy_v(0, start, last - start);
+    }
 
     const T* qp = static_cast<const T*>(g.q) + b * g.q_b + static_cast<int64_t>(i) * g.q_l +
                   static_cast<int64_t>(head) * g.q_h;
@@ -374,7 +470,10 @@ struct Attention {
     for (int s = 0; s < DS; ++s) {
       const int c = (2 * s + h) * 8;
       v4i z = v4i{0, 0, 0, 0};
-      if (real && c < g.D) z = *reinterpret_cast<const v4i*>(qp + c);
+      if (real && c < g.D && g.q_sign != 0) {
+        z = *reinterpret_cast<const v4i*>(qp + c);
+        if (g.q_sign < 0) z = z ^ static_cast<int>(0x80008000u);
+      }
       qf[s] = __builtin_bit_cast(vec, z);
     }
 #pragma unroll
@@ -383,17 +482,24 @@ struct Attention {
       for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
     m = kNegInf;
     l = 0.f;
+    large = false;
 
     for (int tt = t0; tt < t1; ++tt) {
-      const int key0 = first + tt * KT;
-      const int s = (tt - t0) & 1;
+      const int key0 = first + tt * KT, s = (tt - t0) & 1;
       __builtin_amdgcn_s_waitcnt(wait_vmem(0));
       __syncthreads();                 // the tile is in stage s, stage s ^ 1 is free
-      if (tt + 1 < t1) copy(s ^ 1, key0 + KT, last - (key0 + KT));
-      const int k0 = key0 + 32 * KB * kw, k1 = k0 + 32 * KB;   // this wave's keys
+      if (tt + 1 < t1) {
+        copy_k(s ^ 1, key0 + KT, last - (key0 + KT));
+        copy_v(s ^ 1, key0 + KT, last - (key0 + KT));
+      }
+      const int row0 = 32 * KB * kw, k0 = key0 + row0, k1 = k0 + 32 * KB;   // this wave's keys
       if (k1 <= w_lo || k0 >= w_hi) continue;
-      if (k0 >= w_lo_max && k1 <= w_hi_min) tile<false>(s, key0);
-      else tile<true>(s, key0);
+      int kb = 0;
+      if constexpr (KB == 2) {
+        if (k0 >= w_lo_max && k1 <= w_hi_min) kb = pair(s, row0, k0);
+      }
+#pragma unroll 1
+      for (; kb < KB; ++kb) block(s, row0 + 32 * kb, k0 + 32 * kb);
     }
     l = half_sum(l);
     if constexpr (KW > 1) join_waves();

@@ -20,8 +20,10 @@ struct AttnArgs {
   int64_t range_b;           // batch stride of ranges (elements; 0: shared)
   float* part_ml;            // splits: maximum and sum per row
   float* part_o;             // splits: unnormalized outputs, D per row
-  float scale2;              // scale * log2(e)
-  float cap_in, cap2;        // 2 log2(e) scale / cap, cap * log2(e); cap2 0: no cap
+  // the kernel's scale is positive: its sign, or 0, goes into Q
+  int q_sign;
+  float scale2;              // |scale| * log2(e), 1 for a scale of 0
+  float cap_in, cap2;        // 2 log2(e) |scale| / cap, cap * log2(e); cap2 0: no cap
   int B, Lq, Lk, Hkv, G, D;  // G query heads per key head
   int rows;                  // Lq * G
   int causal;

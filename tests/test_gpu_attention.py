@@ -157,6 +157,25 @@ def test_scores_of_the_lowest_value(sq):
     check(sq, q, k, v, softcap=5.0, scale=1.0)
 
 
+@pytest.mark.parametrize("kw", [{}, dict(softcap=4.0)])
+def test_negative_and_zero_scale(sq, kw):
+    q, k, v = qkv(1, 70, 200, 2, 2, 64, BF16)
+    check(sq, q, k, v, scale=-0.3, **kw)
+    check(sq, q, k, v, scale=0.0, causal=True, **kw)
+
+
+def test_logits_that_grow_along_the_keys(sq):
+    """Each block of keys outgrows the reference maximum of the one before, slowly,
+    suddenly, and beyond what one rounding of scale times score would survive."""
+    q, k, v = qkv(1, 130, 512, 1, 1, 128, BF16)
+    ramp = torch.arange(512, device="cuda")[None, :, None, None]
+    check(sq, q, (k * (1 + ramp / 32)).to(BF16), v)
+    check(sq, q, (k * torch.where(ramp % 96 < 32, 1.0, 40.0)).to(BF16), v)
+    check(sq, q, (k * torch.where(ramp < 300, 1.0, 3e4)).to(BF16), v, scale=10.0)
+    check(sq, q, (k * torch.where(ramp < 300, 1.0, 1e30)).to(BF16), v)
+    check(sq, (q * 1e30).to(BF16), k, v)
+
+
 @pytest.mark.parametrize("Lq,Lk,Hq,Hkv", [(1, 5000, 8, 2), (3, 3000, 4, 4), (128, 4096, 2, 1), (260, 2100, 1, 1)])
 def test_split_along_the_keys(sq, Lq, Lk, Hq, Hkv):
     """With the workspace the keys are split over workgroups, without it they are not."""
