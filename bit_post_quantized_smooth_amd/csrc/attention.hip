@@ -136,7 +136,8 @@ struct Attention {
   bool large;                                       // a reference beyond kLarge
   int w_lo, w_hi, w_lo_max, w_hi_min;               // over the wave's rows
   float slope2;
-  uint32_t koff[CPW], voff[CPW];
+  int kb0, vb0;                                     // k_base(), v_base()
+  uint32_t krow, vrow, unit_at[CPW];                // a lane's share of the copies
 
   __device__ __forceinline__ Attention(const AttnArgs& args, Lds& shared) : g(args), lds(shared) {}
 
@@ -147,7 +148,8 @@ struct Attention {
         make_buffer(base, static_cast<uint32_t>(((n - 1) * g.k_l + g.D) * 2));
 #pragma unroll
     for (int i = 0; i < CPW; ++i)
-      buffer_to_lds16(buf, &lds.k[s][(CPW * wave + i) * RPC][0], koff[i], 0);
+      buffer_to_lds16(buf, &lds.k[s][(CPW * wave + i) * RPC][0], krow + unit_at[i],
+                      static_cast<uint32_t>(i * RPC * 2 * g.k_l));
   }
   __device__ __forceinline__ void copy_v(int s, int key0, int keys) {
     const char* base = static_cast<const char*>(g.v) + (b * g.v_b + hk * g.v_h + key0 * g.v_l) * 2;
@@ -156,7 +158,8 @@ struct Attention {
         make_buffer(base, static_cast<uint32_t>(((n - 1) * g.v_l + g.D) * 2));
 #pragma unroll
     for (int i = 0; i < CPW; ++i)
-      buffer_to_lds16(buf, &lds.v[s][(CPW * wave + i) * RPC][0], voff[i], 0);
+      buffer_to_lds16(buf, &lds.v[s][(CPW * wave + i) * RPC][0], vrow + unit_at[i],
+                      static_cast<uint32_t>(i * RPC * 2 * g.v_l));
   }
 
   // Unit u of row r lies at u ^ twist(r). LDS has 64 banks of 4 bytes. A read of
@@ -168,36 +171,49 @@ struct Attention {
     return UNITS == 16 ? 4 * (r & 3) + ((r >> 2) & 3) : 2 * (r & 2) + ((r >> 2) & 3);
   }
 
-  // The V^T operand of 16 keys (from key on) and output block d: lane (d, h)
-  // gets keys 4h .. 4h+3 and 8+4h .. 8+4h+3 of channel 32 d + lane % 32.
-  __device__ __forceinline__ v8s v_frag(int s, int key, int d) {
-    const int a = lane & 15, g16 = lane >> 4;
-    const int ch = 32 * d + 16 * (g16 & 1) + 4 * (a & 3);
-    v4s part[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int row = key + 8 * e + 4 * (g16 >> 1) + (a >> 2);
-      const int unit = (ch >> 3) ^ twist(row);
-      const uint8_t* p = &lds.v[s][row][unit * 16 + (ch & 4) * 2];
-      part[e] = read_tr(p);
-    }
-    return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  // Addresses within a stage. Rows are 2 * DP bytes and a multiple of 16 rows
+  // apart the twist is the same, so all operands of a tile come from two base
+  // addresses per lane: the unit's bits are flipped by constants and whole groups
+  // of rows are added. (Kept in registers each, they would not fit beside the
+  // outputs; opaque() stops the compiler from doing that.)
+  static __device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+  }
+  __device__ __forceinline__ int k_at(int s) const { return opaque(kb0 + s * KT * DP * 2); }
+  __device__ __forceinline__ int v_at(int s) const { return opaque(vb0 + s * KT * DP * 2); }
+  // K: row rl, unit h.
+  __device__ __forceinline__ int k_base() const { return rl * DP * 2 + ((h ^ twist(rl)) << 4); }
+  // V: row 4h + a/4, the 4 channels at 16 * (group & 1) + 4 * (a & 3), a = lane % 16.
+  __device__ __forceinline__ int v_base() const {
+    const int a = lane & 15, row = 4 * h + (a >> 2), ch = (lane & 16) + 4 * (a & 3);
+    return row * DP * 2 + (((ch >> 3) ^ twist(row)) << 4) + (ch & 4) * 2;
+  }
+
+  // The V^T operand of 16 keys (from LDS row `row`, a multiple of 16) and output
+  // block d: lane (d, h) gets keys 4h .. 4h+3 and 8+4h .. 8+4h+3 of channel 32 d +
+  // lane % 32. at: the stage's base address.
+  __device__ __forceinline__ v8s v_frag(int at, int row, int d) const {
+    const uint8_t* p = &lds.v[0][0][0] + row * DP * 2;
+    // rows 8 apart differ in one bit of their twist
+    const v4s lo4 = read_tr(p + (at ^ (d * 64)));
+    const v4s hi4 = read_tr(p + 8 * DP * 2 + (at ^ (d * 64) ^ 32));
+    return __builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 
   // Without a cap and slopes a score stays as the products give it and its scale
   // goes into the exponential; with them it is made a base-2 logit here.
   static constexpr bool RAW = !CAP && !SLOPES;
 
-  // x = K Q^T of the 32 keys from LDS row `row0` on, in stage s
-  __device__ __forceinline__ v16f products(int s, int row0) {
+  // x = K Q^T of the 32 keys from LDS row `row0` on; at: the stage's base address
+  __device__ __forceinline__ v16f products(int at, int row0) {
     v16f x;
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    const int row = row0 + rl;
+    const uint8_t* p = &lds.k[0][0][0] + row0 * DP * 2;
 #pragma unroll
     for (int t = 0; t < DS; ++t) {
-      const int unit = (2 * t + h) ^ twist(row);
-      const v4i kf = *reinterpret_cast<const v4i*>(&lds.k[s][row][unit * 16]);
+      const v4i kf = *reinterpret_cast<const v4i*>(p + (at ^ (t * 32)));
       x = Half<T>::mfma(__builtin_bit_cast(vec, kf), qf[t], x);
     }
     return x;
@@ -264,13 +280,13 @@ struct Attention {
     }
   }
 
-  // O^T += V^T P^T over the 32 keys from row0 on in stage s, every key seen
-  __device__ __forceinline__ void pv(int s, int row0, const vec (&p)[2]) {
+  // O^T += V^T P^T over the 32 keys from row0 on, every key seen
+  __device__ __forceinline__ void pv(int at, int row0, const vec (&p)[2]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int d = 0; d < DB; ++d)
-        o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v_frag(s, row0 + 16 * t, d)), p[t], o[d]);
+        o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v_frag(at, row0 + 16 * t, d)), p[t], o[d]);
   }
 
   // The same where masks hide keys from some rows. A hidden key has P = 0, but 0
@@ -278,7 +294,7 @@ struct Attention {
   // the operands are looked through first; where there is such a value it is
   // taken out of the operand, and add_special() brings it to the rows that do see
   // its key.
-  __device__ __forceinline__ void pv_masked(int s, int row0, int key0, const vec (&p)[2]) {
+  __device__ __forceinline__ void pv_masked(int s, int at, int row0, int key0, const vec (&p)[2]) {
     bool special = false;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -286,7 +302,7 @@ struct Attention {
       v8u big = v8u{0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
-        v[d] = v_frag(s, row0 + 16 * t, d);
+        v[d] = v_frag(at, row0 + 16 * t, d);
         big = __builtin_elementwise_max(big, __builtin_bit_cast(v8u, v[d] & short{0x7FFF}));
       }
       uint16_t most = 0;
@@ -334,12 +350,12 @@ struct Attention {
   // One block of 32 keys, whose first row in stage s is row0 and first key key0,
   // masked, with logits of any size.
   __device__ __forceinline__ void block(int s, int row0, int key0) {
-    v16f x = products(s, row0);
+    v16f x = products(k_at(s), row0);
     const float top = half_max(logits<true>(x, key0));
     if (outgrows(top)) raise(top);
     vec p[2];
     exponentials<false>(x, p);
-    pv_masked(s, row0, key0, p);
+    pv_masked(s, v_at(s), row0, key0, p);
   }
 
   // The wave's two blocks of a tile that every row sees whole: the softmax of one
@@ -347,11 +363,12 @@ struct Attention {
   // cores. A block that outgrows the reference, and logits too large for the
   // fused exponential, are left to block(). Returns the blocks done.
   __device__ __forceinline__ int pair(int s, int row0, int key0) {
-    v16f x = products(s, row0);
+    const int ka = k_at(s), va = v_at(s);
+    v16f x = products(ka, row0);
     vec p[2], r[2];
     if (outgrows(half_max(logits<false>(x, key0))) || (RAW && large)) return 0;
     __builtin_amdgcn_sched_barrier(0);
-    v16f y = products(s, row0 + 32);
+    v16f y = products(ka, row0 + 32);
     exponentials<true>(x, p);
 #pragma unroll
     for (int i = 0; i < DS; ++i) {
@@ -361,11 +378,11 @@ struct Attention {
     }
     __builtin_amdgcn_sched_barrier(0);
     if (outgrows(half_max(logits<false>(y, key0 + 32)))) {
-      pv(s, row0, p);
+      pv(va, row0, p);
       return 1;
     }
     __builtin_amdgcn_sched_barrier(0);
-    pv(s, row0, p);
+    pv(va, row0, p);
     exponentials<true>(y, r);
 #pragma unroll
     for (int i = 0; i < 2 * DB; ++i) {
@@ -374,7 +391,7 @@ struct Attention {
       __builtin_amdgcn_sched_group_barrier(0x002, 28 / DB, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
-    pv(s, row0 + 32, r);
+    pv(va, row0 + 32, r);
     return 2;
   }
 
@@ -450,13 +467,17 @@ struct Attention {
     const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / g.splits);
     const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / g.splits);
 
+    kb0 = k_base();
+    vb0 = v_base();
+    // the first of the wave's rows that this lane copies; units past D (a multiple
+    // of 8 channels) get an offset beyond any buffer
+    const int copied = CPW * wave * RPC + lane / UNITS;
+    krow = static_cast<uint32_t>(copied * g.k_l * 2);
+    vrow = static_cast<uint32_t>(copied * g.v_l * 2);
 #pragma unroll
     for (int c = 0; c < CPW; ++c) {
-      const int row = (CPW * wave + c) * RPC + lane / UNITS;
-      const int unit = (lane % UNITS) ^ twist(row);
-      const bool in = unit * 8 < g.D;               // D is a multiple of 8
-      koff[c] = in ? static_cast<uint32_t>((row * g.k_l + unit * 8) * 2) : 0xFFFFFFF0u;
-      voff[c] = in ? static_cast<uint32_t>((row * g.v_l + unit * 8) * 2) : 0xFFFFFFF0u;
+      const int unit = (lane % UNITS) ^ twist(copied + c * RPC);
+      unit_at[c] = unit * 8 < g.D ? static_cast<uint32_t>(unit * 16) : 0x80000000u;
     }
     const int start = first + t0 * KT;
     if (t0 < t1) {
