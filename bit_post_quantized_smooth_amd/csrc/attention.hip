@@ -115,6 +115,7 @@ struct Attention {
     uint8_t k[2][KT][DP * 2];
     uint8_t v[2][KT][DP * 2];
     int bounds[kWaves][2];
+    int odd[kWaves];
   };
   static_assert(KW == 1 || sizeof(Lds::k) + sizeof(Lds::v) >=
                                static_cast<size_t>(kWaves) * 32 * (DP + 2) * 4,
@@ -249,7 +250,7 @@ struct Attention {
   __device__ __forceinline__ bool outgrows(float top) const {
     return __builtin_amdgcn_ballot_w64(top > m + kGrow) != 0;
   }
-  __device__ __forceinline__ void raise(float top) {
+  __device__ __forceinline__ float raise(float top) {
     const float m_new = fmaxf(m, top);
     const float alpha = m_new == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
     m = m_new;
@@ -259,22 +260,26 @@ struct Attention {
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][i] = o[d][i] * alpha;
+    return alpha;                        // what everything under the old reference is worth
   }
   // what the exponentials subtract; -inf: a row that has seen no key yet
   __device__ __forceinline__ float base() const { return m == kNegInf ? 0.f : m; }
 
-  // x -> P in 16 bits (the operands of 16 keys each), and their sum. FUSED: scale
-  // * x - base in one rounding. That leaves a factor of the row, from the rounding
-  // of base, which the division by the sum takes out, unless base is so large
-  // that the factor overflows: then the product is rounded as base was.
-  template <bool FUSED>
-  __device__ __forceinline__ void exponentials(const v16f& x, vec (&p)[2]) {
+  // x -> P in 16 bits (the operands of 16 keys each), and their sum. scale * x -
+  // base takes one rounding. That leaves a factor of the row, from the rounding of
+  // base, which the division by the sum takes out, unless base is so large that
+  // the factor overflows: then the product is rounded first, as base was.
+  __device__ __forceinline__ void exponentials(v16f& x, vec (&p)[2]) {
     const float sub = base();
+    float scale = g.scale2;
+    if (RAW && large) {
+      scale = 1.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = x[i] * g.scale2;
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float e = __builtin_amdgcn_exp2f(!RAW    ? x[i] - sub
-                                             : FUSED ? __builtin_fmaf(x[i], g.scale2, -sub)
-                                                     : x[i] * g.scale2 - sub);
+      const float e = __builtin_amdgcn_exp2f(RAW ? __builtin_fmaf(x[i], scale, -sub) : x[i] - sub);
       l = l + e;
       p[i >> 3][i & 7] = static_cast<T>(e);
     }
@@ -289,12 +294,9 @@ struct Attention {
         o[d] = Half<T>::mfma(__builtin_bit_cast(vec, v_frag(at, row0 + 16 * t, d)), p[t], o[d]);
   }
 
-  // The same where masks hide keys from some rows. A hidden key has P = 0, but 0
-  // times an infinity or a NaN in V would reach the rows that do not see it. So
-  // the operands are looked through first; where there is such a value it is
-  // taken out of the operand, and add_special() brings it to the rows that do see
-  // its key.
-  __device__ __forceinline__ void pv_masked(int s, int at, int row0, int key0, const vec (&p)[2]) {
+  // The same with the infinities and NaN of V taken out of the operands;
+  // add_special() brings them to the rows that see their keys.
+  __device__ __forceinline__ void pv_careful(int s, int at, int row0, int key0, const vec (&p)[2]) {
     bool special = false;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -347,52 +349,119 @@ struct Attention {
     }
   }
 
-  // One block of 32 keys, whose first row in stage s is row0 and first key key0,
-  // masked, with logits of any size.
+  // One block of 32 keys, whose first row in stage s is row0 and first key key0.
+  template <bool CAREFUL>
   __device__ __forceinline__ void block(int s, int row0, int key0) {
     v16f x = products(k_at(s), row0);
     const float top = half_max(logits<true>(x, key0));
     if (outgrows(top)) raise(top);
     vec p[2];
-    exponentials<false>(x, p);
-    pv_masked(s, v_at(s), row0, key0, p);
+    exponentials(x, p);
+    if constexpr (CAREFUL) pv_careful(s, v_at(s), row0, key0, p);
+    else pv(v_at(s), row0, p);
   }
 
-  // The wave's two blocks of a tile that every row sees whole: the softmax of one
-  // block runs on the vector unit beside the products of the other on the matrix
-  // cores. A block that outgrows the reference, and logits too large for the
-  // fused exponential, are left to block(). Returns the blocks done.
-  __device__ __forceinline__ int pair(int s, int row0, int key0) {
+  // Two blocks: the softmax of one runs on the vector unit beside the products of
+  // the other on the matrix cores. The branches are rare and change registers in
+  // place, so that the outputs stay where they are.
+  template <bool MASK>
+  __device__ __forceinline__ void pair(int s, int row0, int key0) {
     const int ka = k_at(s), va = v_at(s);
     v16f x = products(ka, row0);
     vec p[2], r[2];
-    if (outgrows(half_max(logits<false>(x, key0))) || (RAW && large)) return 0;
+    float top = half_max(logits<MASK>(x, key0));
+    if (outgrows(top)) raise(top);
     __builtin_amdgcn_sched_barrier(0);
     v16f y = products(ka, row0 + 32);
-    exponentials<true>(x, p);
+    exponentials(x, p);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
     for (int i = 0; i < DS; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x002, 56 / DS, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (outgrows(half_max(logits<false>(y, key0 + 32)))) {
-      pv(va, row0, p);
-      return 1;
+    top = half_max(logits<MASK>(y, key0 + 32));
+    if (outgrows(top)) {                 // x's exponentials are not in o yet
+      const float alpha = raise(top);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        p[i >> 3][i & 7] = static_cast<T>(static_cast<float>(p[i >> 3][i & 7]) * alpha);
     }
     __builtin_amdgcn_sched_barrier(0);
     pv(va, row0, p);
-    exponentials<true>(y, r);
+    exponentials(y, r);
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
     for (int i = 0; i < 2 * DB; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
       __builtin_amdgcn_sched_group_barrier(0x002, 28 / DB, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
     pv(va, row0 + 32, r);
-    return 2;
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // Tiles t0 .. t1-1 of the keys from `first` on, the first of them on its way to
+  // stage 0, into o, m and l.
+  template <bool CAREFUL>
+  __device__ __forceinline__ void pass(int first, int last, int t0, int t1) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+    m = kNegInf;
+    l = 0.f;
+    large = false;
+    // The wave's keys of tile tt are f + tt * KT .. + 32 * KB - 1. It has no part in
+    // tiles before `on` and from `off` on; every row sees all of its keys in tiles
+    // `in` .. `out` - 1. A loop for each: with one loop and branches the outputs
+    // are copied where the paths meet.
+    const int row0 = 32 * KB * kw, f = first + row0;
+    auto upto = [&](int x) {           // tiles that begin before key x, within t0 .. t1
+      const int n = x > f ? (x - f + KT - 1) / KT : 0;
+      return n < t0 ? t0 : n < t1 ? n : t1;
+    };
+    const int on = upto(w_lo + 1 - 32 * KB), off = max(on, upto(w_hi));
+    int in = max(on, upto(w_lo_max)), out = min(off, upto(w_hi_min - 32 * KB + 1));
+    if (CAREFUL || KB != 2 || in >= out) in = out = off;
+    int tt = t0;
+    auto begin = [&]() {
+      const int key0 = first + tt * KT, s = (tt - t0) & 1;
+      __builtin_amdgcn_s_waitcnt(wait_vmem(0));
+      __syncthreads();                 // the tile is in stage s, stage s ^ 1 is free
+      if (tt + 1 < t1) {
+        copy_k(s ^ 1, key0 + KT, last - (key0 + KT));
+        copy_v(s ^ 1, key0 + KT, last - (key0 + KT));
+      }
+      return s;
+    };
+    auto masked = [&]() {
+      const int s = begin();
+      if constexpr (KB == 2 && !CAREFUL) {
+        pair<true>(s, row0, f + tt * KT);
+      } else {
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb)
+          block<CAREFUL>(s, row0 + 32 * kb, f + tt * KT + 32 * kb);
+      }
+    };
+    for (; tt < on; ++tt) begin();
+    for (; tt < in; ++tt) masked();
+    if constexpr (KB == 2 && !CAREFUL) {
+      for (; tt < out; ++tt) pair<false>(begin(), row0, f + tt * KT);
+      for (; tt < off; ++tt) masked();
+    }
+    for (; tt < t1; ++tt) begin();
+    __syncthreads();                   // the tiles are no longer read
   }
 
   __device__ __forceinline__ void run() {
@@ -497,30 +566,27 @@ struct Attention {
       }
       qf[s] = __builtin_bit_cast(vec, z);
     }
+    // A hidden key has P = 0, but 0 times an infinity or a NaN in V would reach the
+    // rows that do not see it. That leaves a NaN, so the first pass does not look
+    // at V; only where an output is not finite a second one does.
+    pass<false>(first, last, t0, t1);
+    bool odd = false;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
-    m = kNegInf;
-    l = 0.f;
-    large = false;
-
-    for (int tt = t0; tt < t1; ++tt) {
-      const int key0 = first + tt * KT, s = (tt - t0) & 1;
-      __builtin_amdgcn_s_waitcnt(wait_vmem(0));
-      __syncthreads();                 // the tile is in stage s, stage s ^ 1 is free
-      if (tt + 1 < t1) {
-        copy_k(s ^ 1, key0 + KT, last - (key0 + KT));
-        copy_v(s ^ 1, key0 + KT, last - (key0 + KT));
+      for (int e = 0; e < 16; ++e) odd |= !(fabsf(o[d][e]) < __builtin_inff());
+    const bool again = __builtin_amdgcn_ballot_w64(odd) != 0;
+    if (lane == 0) lds.odd[wave] = again;
+    __syncthreads();
+    bool any = false;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) any |= lds.odd[w] != 0;
+    if (__builtin_amdgcn_readfirstlane(any)) {
+      if (t0 < t1) {
+        copy_k(0, start, last - start);
+        copy_v(0, start, last - start);
       }
-      const int row0 = 32 * KB * kw, k0 = key0 + row0, k1 = k0 + 32 * KB;   // this wave's keys
-      if (k1 <= w_lo || k0 >= w_hi) continue;
-      int kb = 0;
-      if constexpr (KB == 2) {
-        if (k0 >= w_lo_max && k1 <= w_hi_min) kb = pair(s, row0, k0);
-      }
-#pragma unroll 1
-      for (; kb < KB; ++kb) block(s, row0 + 32 * kb, k0 + 32 * kb);
+      pass<true>(first, last, t0, t1);
     }
     l = half_sum(l);
     if constexpr (KW > 1) join_waves();
@@ -532,7 +598,6 @@ struct Attention {
   __device__ __forceinline__ void join_waves() {
     float* mem = reinterpret_cast<float*>(&lds);
     float* ml = mem + kWaves * 32 * DP;
-    __syncthreads();                   // the tiles are no longer read
     if (h == 0) {
       ml[(wave * 32 + rl) * 2] = m;
       ml[(wave * 32 + rl) * 2 + 1] = l;
