@@ -251,7 +251,7 @@ size_t svdq_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t
   const int s = check_attention_sizes("svdq_attention_workspace_bytes", B, Lq, Lk, Hq, Hkv, D);
   clear_error();                       // a size query reports by its 0 alone
   if (s != SVDQ_OK || B == 0 || Lq == 0) return 0;
-  return attention_bytes(B, Lq, Hq, D, attention_plan(B, Lq, Lk, Hq, Hkv, true).splits);
+  return attention_bytes(B, Lq, Hq, D, attention_plan(B, Lq, Lk, Hq, Hkv, D, true).splits);
 }
 
 int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int dtype, int64_t B,
@@ -283,9 +283,9 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
     return fail(SVDQ_ERR_ALIGN, fn,
                 "Q, K, V, Out and the workspace must be 16-byte aligned, the rest 4-byte");
   if (int s = device_ready(fn)) return s;
-  AttnPlan p = attention_plan(B, Lq, Lk, Hq, Hkv, true);
+  AttnPlan p = attention_plan(B, Lq, Lk, Hq, Hkv, D, true);
   if (p.splits > 1 && (ws == nullptr || ws_bytes < attention_bytes(B, Lq, Hq, D, p.splits)))
-    p = attention_plan(B, Lq, Lk, Hq, Hkv, false);
+    p = attention_plan(B, Lq, Lk, Hq, Hkv, D, false);
   if (p.wgs > kMaxRows) return fail(SVDQ_ERR_SHAPE, fn, "too many rows");
   AttnArgs g{};
   g.q = Q;

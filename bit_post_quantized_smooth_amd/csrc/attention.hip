@@ -33,6 +33,8 @@
 // that joins them in order.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "../../include/svdq.h"
 #include "attention.hpp"
 #include "block_common.hpp"
@@ -675,35 +677,64 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(const AttnArg
   a.run();
 }
 
-// Joins the splits of one output row per 16 lanes: 8 channels per lane.
+// Joins the splits of one output row in a workgroup: 32 lanes hold its channels,
+// 4 each, and 8 groups of lanes take the splits in turn; their sums are added in
+// order. Every load is issued before the first is needed, the row being short.
+constexpr int kJoin = 8;
+constexpr int kMaxSplits = 64;
+
 template <class T>
-__global__ __launch_bounds__(256) void attention_join(const AttnArgs g) {
+__global__ __launch_bounds__(32 * kJoin) void attention_join(const AttnArgs g) {
+  __shared__ v4f sums[kJoin][32];
+  __shared__ float weights[kJoin];
   const int64_t all = static_cast<int64_t>(g.B) * g.Hkv * g.rows;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
-  const int ch = 8 * (threadIdx.x % 16);
-  if (row >= all || ch >= g.D) return;
-  float top = kNegInf;
-  for (int s = 0; s < g.splits; ++s) top = fmaxf(top, g.part_ml[2 * (s * all + row)]);
-  const float base = top == kNegInf ? 0.f : top;
-  float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < g.splits; ++s) {
-    const float ls = g.part_ml[2 * (s * all + row) + 1];
-    if (ls == 0.f) continue;
-    const float f = __builtin_amdgcn_exp2f(g.part_ml[2 * (s * all + row)] - base);
-    l = __builtin_fmaf(ls, f, l);
-    const float* p = g.part_o + (s * all + row) * g.D + ch;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(p[e], f, o[e]);
+  const int64_t row = blockIdx.x;
+  const int group = threadIdx.x / 32, ch = 4 * (threadIdx.x % 32);
+  // the row's maxima and sums, one split per lane
+  const int lane = threadIdx.x % 64;
+  float m = kNegInf, l = 0.f;
+  if (lane < g.splits) {
+    m = g.part_ml[2 * (lane * all + row)];
+    l = g.part_ml[2 * (lane * all + row) + 1];
   }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  float top = m;
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
+  const float f = l == 0.f ? 0.f : __builtin_amdgcn_exp2f(m - (top == kNegInf ? 0.f : top));
+  v4f o = v4f{0.f, 0.f, 0.f, 0.f};
+  float n = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / kJoin; ++i) {
+    const int s = group + i * kJoin;
+    const float fs = __shfl(f, s), ls = __shfl(l, s);
+    if (s >= g.splits || ls == 0.f) continue;      // nothing was written for it
+    n = __builtin_fmaf(ls, fs, n);
+    if (ch < g.D) {
+      const v4f p = *reinterpret_cast<const v4f*>(g.part_o + (s * all + row) * g.D + ch);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(p[e], fs, o[e]);
+    }
+  }
+  sums[group][threadIdx.x % 32] = o;
+  if (threadIdx.x % 32 == 0) weights[group] = n;
+  __syncthreads();
+  if (group != 0 || ch >= g.D) return;
+#pragma unroll
+  for (int i = 1; i < kJoin; ++i) {
+    const v4f p = sums[i][threadIdx.x];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = o[e] + p[e];
+    n = n + weights[i];
+  }
+  const float inv = n == 0.f ? 0.f : 1.0f / n;
   const int64_t r = row % g.rows, bh = row / g.rows;
   const int64_t b = bh / g.Hkv, hk = bh % g.Hkv;
   T* op = static_cast<T*>(g.out) + b * g.o_b + (r / g.G) * g.o_l + (hk * g.G + r % g.G) * g.o_h + ch;
-  typedef T vec8 __attribute__((ext_vector_type(8)));
-  vec8 y;
+  typedef T vec4 __attribute__((ext_vector_type(4)));
+  vec4 y;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = static_cast<T>(o[e] * inv);
-  *reinterpret_cast<vec8*>(op) = y;
+  for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(o[e] * inv);
+  *reinterpret_cast<vec4*>(op) = y;
 }
 
 template <class T, int DP, int RW, bool CAP>
@@ -731,28 +762,54 @@ hipError_t launch_t(const AttnArgs& g, const AttnPlan& p, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(g.B) * g.Hkv * g.rows;
-  hipLaunchKernelGGL(attention_join<T>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0,
+  hipLaunchKernelGGL(attention_join<T>, dim3(static_cast<unsigned>(rows)), dim3(32 * kJoin), 0,
                      stream, g);
   return hipGetLastError();
 }
 
 }  // namespace
 
-AttnPlan attention_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, bool split) {
+// The split along the keys of least estimated time, in microseconds measured at
+// D = 128: a tile of a workgroup that has its compute unit to itself takes 1.8
+// (128 keys, few rows) or 1.2 (64 keys, 128 rows); few rows are bound by memory
+// from about 150 workgroups on, 128 rows share their unit beyond one workgroup
+// each; a workgroup's start and end take 2.5, and joining splits 4 and their
+// outputs written and read at 4 TB/s. One token, 32 heads over 8, 8 caches of 8191:
+// 55 us with 4 splits, 124 with one, 65 with 16; one cache: 17, 78 (32 splits).
+AttnPlan attention_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D,
+                        bool split) {
   AttnPlan p{};
   const int64_t rows = Lq * (Hq / Hkv);
   p.few = rows <= 32;
   p.row_tiles = (rows + (p.few ? 31 : 127)) / (p.few ? 32 : 128);
   const int64_t wgs = p.row_tiles * B * Hkv;
-  int64_t s = 1;
-  if (split) {
-    s = resident_slots() / (wgs > 0 ? wgs : 1);
-    const int64_t most = Lk / 256;      // at least 256 keys per workgroup
-    s = s > most ? most : s;
-    s = s < 1 ? 1 : s > 64 ? 64 : s;
+  const int64_t tiles = (Lk + (p.few ? 127 : 63)) / (p.few ? 128 : 64);
+  const int cus = resident_slots() / 2;
+  const int slots = p.few && D > 64 ? cus : 2 * cus;
+  float least = -1.f;
+  p.splits = 1;
+  constexpr int kTried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+  for (const int s : kTried) {
+    if (!split || s > kMaxSplits || (s > 1 && s > tiles)) break;
+    const float all = static_cast<float>(wgs) * static_cast<float>(s);
+    const float active = all < slots ? all : static_cast<float>(slots);
+    const float rounds = std::ceil(all / static_cast<float>(slots));
+    float tile;
+    if (p.few) {
+      tile = 0.0124f * active * (D > 64 ? 1.f : 0.5f);
+      if (tile < 1.8f) tile = 1.8f;
+    } else {
+      tile = active <= cus ? 1.2f : 1.2f + 1.3f * (active - cus) / cus;
+    }
+    float us = rounds * (static_cast<float>((tiles + s - 1) / s) * tile + 2.5f);
+    if (s > 1)
+      us += 4.f + static_cast<float>(B * Lq) * static_cast<float>(Hq * D) * s * 8.f / 4e6f;
+    if (least < 0.f || us < least) {
+      least = us;
+      p.splits = s;
+    }
   }
-  p.splits = static_cast<int>(s);
-  p.wgs = wgs * s;
+  p.wgs = wgs * p.splits;
   p.grid = static_cast<unsigned>(p.wgs);
   return p;
 }
