@@ -958,13 +958,14 @@ _E4M3 = ("uint8", "int8", "float8_e4m3fn")
 
 
 def _dt_block(t) -> int:
-    torch = _torch()
-    return BF16 if t.dtype == torch.bfloat16 else _dt(t)
+    d = t.dtype
+    return BF16 if d is _lib.torch.bfloat16 else F16 if d is _lib.torch.float16 else F32
 
 
 def _ld(t) -> int:
     """Row stride of a checked matrix (one row may have any)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    rows, cols = t.shape
+    return t.stride()[0] if rows > 1 else cols or 1
 
 
 def _fp8_side(name, rows, Kp, codes, scales, srows):
@@ -979,21 +980,28 @@ def rmsnorm_quantize_fp8(X, residual, gain, eps: float, a_codes, a_scales, resid
     gain (may be None) as e4m3 codes (M x fp8_padded(K)) and fp32 scales (M x
     fp8_padded(K)/128)."""
     _mat("X", X, None, None, _BLOCK_X)
-    M, K = X.shape
+    shape, dtype = X.shape, X.dtype
+    M, K = shape
     for name, t in (("residual", residual), ("residual_out", residual_out)):
-        if t is not None:
+        if t is not None and not (t.__class__ is X.__class__ and t.dtype is dtype
+                                  and t.shape == shape and t.is_contiguous()):
             _mat(name, t, M, K, _BLOCK_X)
-            if t.dtype != X.dtype:
-                raise ValueError(f"{name}: dtype {t.dtype}, X has {X.dtype}")
+            if t.dtype != dtype:
+                raise ValueError(f"{name}: dtype {t.dtype}, X has {dtype}")
     if gain is not None:
         _buf("gain", gain, _F32, nbytes=4 * K)
-    _fp8_side("a", M, fp8_padded(K), a_codes, a_scales, M)
+    Kp = -(-K // FP8_BLOCK) * FP8_BLOCK
+    _buf("a_codes", a_codes, _E4M3, nbytes=M * Kp)
+    _buf("a_scales", a_scales, _F32, nbytes=M * Kp // (FP8_BLOCK // 4))
     _on_gpu(X, residual, residual_out, gain, a_codes, a_scales)
-    check(lib.svdq_rmsnorm_quantize_fp8(
-        _tp(X), _tp(residual), _dt_block(X), M, K, _ld(X), _ld(residual) if residual is not None
-        else 0, _tp(gain), float(eps), _tp(a_codes), _tp(a_scales), _tp(residual_out),
-        _ld(residual_out) if residual_out is not None else 0, _stream(stream)),
-        "svdq_rmsnorm_quantize_fp8")
+    status = lib.svdq_rmsnorm_quantize_fp8(
+        X.data_ptr(), None if residual is None else residual.data_ptr(), _dt_block(X), M, K,
+        _ld(X), 0 if residual is None else _ld(residual),
+        None if gain is None else gain.data_ptr(), eps, a_codes.data_ptr(), a_scales.data_ptr(),
+        None if residual_out is None else residual_out.data_ptr(),
+        0 if residual_out is None else _ld(residual_out), _stream(stream))
+    if status:
+        check(status, "svdq_rmsnorm_quantize_fp8")
 
 
 def quantize_act_fp8(X, a_codes, a_scales, stream=None):
@@ -1027,10 +1035,13 @@ def gemm_fp8(a_codes, a_scales, w_codes, w_scales, bias, Y, ws=None, stream=None
     if ws is not None:
         _buf("ws", ws, _BYTES + _HALF + _F32)
     _on_gpu(a_codes, a_scales, w_codes, w_scales, bias, Y, ws)
-    check(lib.svdq_gemm_fp8(_tp(a_codes), _tp(a_scales), _tp(w_codes), _tp(w_scales), _tp(bias),
-                            _tp(Y), _dt_block(Y), M, N, Kp, _ld(Y), _act(activation), _tp(ws),
-                            0 if ws is None else ws.numel() * ws.element_size(),
-                            _stream(stream)), "svdq_gemm_fp8")
+    status = lib.svdq_gemm_fp8(
+        a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+        None if bias is None else bias.data_ptr(), Y.data_ptr(), _dt_block(Y), M, N, Kp, _ld(Y),
+        _act(activation), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
+        _stream(stream))
+    if status:
+        check(status, "svdq_gemm_fp8")
 
 
 def linear_fp8_workspace_bytes(M: int, K: int, N: int) -> int:
@@ -1063,22 +1074,20 @@ def _heads(name, t, B, L, H, D, dtype):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype not in (torch.float16, torch.bfloat16):
+    if t.dtype is not torch.float16 and t.dtype is not torch.bfloat16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected float16 or bfloat16")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, Q has {dtype}")
-    if t.dim() != 4 or any(w is not None and s != w for s, w in zip(t.shape, (B, L, H, D))):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(B, L, H, D)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
-        raise ValueError(f"{name}: the inner stride must be 1, got {t.stride(3)}")
+    shape = t.shape
+    if len(shape) != 4 or (B is not None and shape[0] != B) or (L is not None and shape[1] != L) \
+            or (H is not None and shape[2] != H) or (D is not None and shape[3] != D):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {(B, L, H, D)}")
+    sb, sl, sh, sd = t.stride()
+    b, l, h, d = shape
+    if d > 1 and sd != 1:
+        raise ValueError(f"{name}: the inner stride must be 1, got {sd}")
     # a dimension of one (or of none) is never stepped over: its stride is free
-    sb, sl, sh, _ = t.stride()
-    if t.numel() and (t.shape[0] == 1 or t.shape[1] == 1 or t.shape[2] == 1):
-        b, l, h, d = t.shape
-        sb, sl, sh = sb if b > 1 else 0, sl if l > 1 else d, sh if h > 1 else 0
-    elif not t.numel():
-        sb, sl, sh = 0, t.shape[3], 0
-    return sb, sl, sh
+    return sb if b > 1 else 0, sl if l > 1 else d, sh if h > 1 else 0
 
 
 def attention(Q, K, V, Out, scale: float | None = None, softcap: float = 0.0, slopes=None,
@@ -1118,11 +1127,15 @@ def attention(Q, K, V, Out, scale: float | None = None, softcap: float = 0.0, sl
         _buf("ws", ws, _BYTES + _HALF + _F32)
     _on_gpu(Q, K, V, Out, slopes, prefix, key_ranges, ws)
     strides = struct.pack("12q", *sq_, *sk, *sv, *so)
-    check(lib.svdq_attention(
-        _tp(Q), _tp(K), _tp(V), _tp(Out), _dt_block(Q), B, Lq, Lk, Hq, Hkv, D, strides,
-        D ** -0.5 if scale is None else float(scale), float(softcap), _tp(slopes),
-        1 if causal else 0, _tp(prefix), _tp(key_ranges), rb, _tp(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "svdq_attention")
+    status = lib.svdq_attention(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), Out.data_ptr(), _dt_block(Q), B, Lq, Lk, Hq,
+        Hkv, D, strides, D ** -0.5 if scale is None else scale, softcap,
+        None if slopes is None else slopes.data_ptr(), 1 if causal else 0,
+        None if prefix is None else prefix.data_ptr(),
+        None if key_ranges is None else key_ranges.data_ptr(), rb,
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _stream(stream))
+    if status:
+        check(status, "svdq_attention")
 
 
 class Linear:

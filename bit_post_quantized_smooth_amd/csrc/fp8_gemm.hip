@@ -40,6 +40,7 @@ namespace svdq {
 
 namespace {
 
+constexpr int kMaxSlices = 16;      // of a product split along K
 constexpr int kChunk = kFp8Block;   // K values per group and matrix instruction
 // vmcnt(n) expcnt(7) lgkmcnt(0)
 constexpr int wait_copies(int n) { return (n & 15) | ((n >> 4) << 14) | 0x70; }
@@ -51,10 +52,13 @@ struct GemmArgs {
   const float* sw;
   const float* bias;
   void* Y;
-  float* part;                      // split along K: [slice][M][N] fp32
+  float* part;                      // split along K: [slice][M][part_ld(N)] fp32
   int64_t M, N, Kp, ldy;
   int slices;
 };
+
+// Row stride of the partial tiles: 4 columns move in one access.
+__host__ __device__ constexpr int64_t part_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
 template <int N, int I = 0, class F>
 __device__ __forceinline__ void static_for(F&& f) {
@@ -450,31 +454,43 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
     for (int i = 0; i < NBM; ++i) {
       const int64_t m = mw + 16 * i + rl;
       if (m >= g.M) continue;
-      float* out = g.part + (slice * g.M + m) * g.N;
+      float* out = g.part + (slice * g.M + m) * part_ld(g.N);
 #pragma unroll
       for (int j = 0; j < NBN; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (nw + 16 * j + e < g.N) out[nw + 16 * j + e] = acc[i][j][e];
+        if (nw + 16 * j < g.N) *reinterpret_cast<v4f*>(out + nw + 16 * j) = acc[i][j];
     }
   }
 }
 
-// Adds the slices' partial sums in slice order and finishes the outputs.
-template <int YT, bool GELU>
-__global__ __launch_bounds__(256) void gemm_fp8_join(const GemmArgs g) {
-  const int64_t per_row = (g.N + 3) / 4;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+// Adds the slices' partial sums in slice order and finishes the outputs. Few
+// outputs of many slices: what it takes is the loads' latency, so SLICES of them
+// are in flight at once (slices past the last read its values and add nothing)
+// and a workgroup is one wave, which spreads them over the most CUs.
+template <int YT, bool GELU, int SLICES>
+__global__ __launch_bounds__(64) void gemm_fp8_join(const GemmArgs g) {
+  const int64_t per_row = part_ld(g.N) / 4;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
+  if (t >= g.M * per_row) return;
   const int64_t m = t / per_row, n = (t - m * per_row) * 4;
-  if (m >= g.M) return;
-  v4f v = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < g.slices; ++s) {
-    const float* p = g.part + (s * g.M + m) * g.N + n;
+  const v4f* p = reinterpret_cast<const v4f*>(g.part) + t;
+  v4f x[SLICES];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < g.N) v[e] = v[e] + p[e];
+  for (int s = 0; s < SLICES; ++s) x[s] = p[(s < g.slices ? s : 0) * g.M * per_row];
+  const v4f b = bias4(g, n);
+  v4f v = x[0];
+#pragma unroll
+  for (int s = 1; s < SLICES; ++s) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = s < g.slices ? v[e] + x[s][e] : v[e];
   }
-  finish4<YT, GELU>(g, v, bias4(g, n), m, n);
+  finish4<YT, GELU>(g, v, b, m, n);
+}
+
+template <int YT, bool GELU>
+void launch_join(const GemmArgs& g, hipStream_t stream) {
+  const unsigned wgs = static_cast<unsigned>((g.M * (part_ld(g.N) / 4) + 63) / 64);
+  if (g.slices <= 4) hipLaunchKernelGGL((gemm_fp8_join<YT, GELU, 4>), dim3(wgs), dim3(64), 0, stream, g);
+  else hipLaunchKernelGGL((gemm_fp8_join<YT, GELU, kMaxSlices>), dim3(wgs), dim3(64), 0, stream, g);
 }
 
 // ---------------------------------------------------------------------------
@@ -571,7 +587,7 @@ GemmPlan least(const TileCost (&tiles)[COUNT], int64_t M, int64_t N, int64_t Kp,
   float least = -1.f;
   for (int t = 0; t < COUNT; ++t) {
     const TileCost& k = tiles[t];
-    for (int s = 1; s <= (split ? 16 : 1) && s * 2 <= C + 1; s *= 2) {
+    for (int s = 1; s <= (split ? kMaxSlices : 1) && s * 2 <= C + 1; s *= 2) {
       const int64_t wgs = ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn) * s;
       const int64_t slots = cus * k.per_cu, rounds = wgs / slots;
       const float chunks = static_cast<float>((C + s - 1) / s);
@@ -630,9 +646,7 @@ hipError_t launch_e(GemmArgs& g, hipStream_t stream) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.slices == 1) return e;
-  const int64_t threads = g.M * ((g.N + 3) / 4);
-  hipLaunchKernelGGL((gemm_fp8_join<YT, GELU>), dim3(static_cast<unsigned>((threads + 255) / 256)),
-                     dim3(256), 0, stream, g);
+  launch_join<YT, GELU>(g, stream);
   return hipGetLastError();
 }
 
@@ -644,7 +658,7 @@ size_t gemm_fp8_split_bytes(int64_t M, int64_t N, int64_t Kp) {
   const int s16 = gemm_plan(M, N, Kp, false, true).slices;
   const int s32 = gemm_plan(M, N, Kp, true, true).slices;
   const int s = s16 > s32 ? s16 : s32;
-  return s > 1 ? static_cast<size_t>(s) * M * N * 4 : 0;
+  return s > 1 ? static_cast<size_t>(s) * M * part_ld(N) * 4 : 0;
 }
 
 hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
