@@ -100,14 +100,13 @@ int check_gemm(const char* fn, const uint8_t* a_codes, const float* a_scales,
 
 // The workspace of svdq_linear_fp8: codes, scales, the split product's partials.
 struct LinearWs {
-  size_t scales, part, total;
+  size_t scales, part;
 };
-LinearWs linear_ws(int64_t M, int64_t K, int64_t N) {
+LinearWs linear_ws(int64_t M, int64_t K) {
   const int64_t Kp = fp8_padded(K);
   LinearWs w;
   w.scales = round_up(static_cast<size_t>(M) * Kp, 256);
   w.part = w.scales + round_up(static_cast<size_t>(M) * (Kp / SVDQ_FP8_BLOCK) * 4, 256);
-  w.total = w.part + gemm_fp8_split_bytes(M, N, Kp);
   return w;
 }
 
@@ -163,16 +162,15 @@ int svdq_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* 
   if (!aligned(ws, 16)) return fail(SVDQ_ERR_ALIGN, fn, "the workspace must be 16-byte aligned");
   if (M == 0) return SVDQ_OK;
   if (int s = device_ready(fn)) return s;
-  const size_t need = gemm_fp8_split_bytes(M, N, Kp);
-  float* part = need > 0 && ws != nullptr && ws_bytes >= need ? static_cast<float*>(ws) : nullptr;
   return check_hip(launch_gemm_fp8(a_codes, a_scales, w_codes, w_scales, bias, Y, y_dtype, M, N, Kp,
-                                   ldy, activation == SVDQ_ACT_GELU_TANH, part, stream),
+                                   ldy, activation == SVDQ_ACT_GELU_TANH, static_cast<float*>(ws),
+                                   ws ? ws_bytes : 0, stream),
                    fn);
 }
 
 size_t svdq_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (M < 1 || K < 1 || N < 1) return 0;
-  return linear_ws(M, K, N).total;
+  return linear_ws(M, K).part + gemm_fp8_split_bytes(M, N, fp8_padded(K));
 }
 
 int svdq_linear_fp8(const void* X, int x_dtype, int64_t ldx, const uint8_t* w_codes,
@@ -190,9 +188,9 @@ int svdq_linear_fp8(const void* X, int x_dtype, int64_t ldx, const uint8_t* w_co
     if (!ws) return fail(SVDQ_ERR_NULL, fn, "null workspace");
     if (!aligned(ws, 256)) return fail(SVDQ_ERR_ALIGN, fn, "workspace must be 256-byte aligned");
   }
-  const LinearWs L = linear_ws(M, K, N);
+  const LinearWs L = linear_ws(M, K);
   if (ws_bytes < L.part) {
-    set_error("%s: workspace %zu bytes < %zu needed", fn, ws_bytes, L.total);
+    set_error("%s: workspace %zu bytes < %zu needed", fn, ws_bytes, L.part);
     return SVDQ_ERR_WORKSPACE;
   }
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -205,14 +203,13 @@ int svdq_linear_fp8(const void* X, int x_dtype, int64_t ldx, const uint8_t* w_co
     return s;
   if (M == 0) return SVDQ_OK;
   if (int s = device_ready(fn)) return s;
-  float* part = L.total > L.part && ws_bytes >= L.total ? reinterpret_cast<float*>(base + L.part)
-                                                        : nullptr;
   if (int s = check_hip(launch_quantize_fp8(X, nullptr, x_dtype, M, K, ldx, 0, false, nullptr, 0.f,
                                             codes, scales, nullptr, 0, stream),
                         fn))
     return s;
   return check_hip(launch_gemm_fp8(codes, scales, w_codes, w_scales, bias, Y, y_dtype, M, N,
-                                   fp8_padded(K), ldy, activation == SVDQ_ACT_GELU_TANH, part,
+                                   fp8_padded(K), ldy, activation == SVDQ_ACT_GELU_TANH,
+                                   reinterpret_cast<float*>(base + L.part), ws_bytes - L.part,
                                    stream),
                    fn);
 }

@@ -20,13 +20,13 @@ hipError_t launch_quantize_fp8(const void* X, const void* residual, int dtype, i
                                float eps, uint8_t* codes, float* scales, void* residual_out,
                                int64_t ldo, hipStream_t stream);
 
-// part: null, or gemm_fp8_split_bytes(M, N, Kp, y_dtype) bytes (16-byte
-// aligned) for the fp32 partial tiles of a product that is split along K;
-// without it every shape runs unsplit.
+// part: part_bytes (16-byte aligned) for the fp32 partial tiles of a product
+// that is split along K; with fewer than gemm_fp8_split_bytes(M, N, Kp), or a
+// null pointer, the product may run unsplit.
 hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
                            const float* w_scales, const float* bias, void* Y, int y_dtype,
                            int64_t M, int64_t N, int64_t Kp, int64_t ldy, bool gelu, float* part,
-                           hipStream_t stream);
+                           size_t part_bytes, hipStream_t stream);
 size_t gemm_fp8_split_bytes(int64_t M, int64_t N, int64_t Kp);
 
 }  // namespace svdq

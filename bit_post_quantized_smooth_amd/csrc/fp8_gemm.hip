@@ -582,14 +582,15 @@ struct GemmPlan {
 // 4608 x 12288 x 3072 the choice is within 4% on 22 and 12% on the others.
 template <int COUNT>
 GemmPlan least(const TileCost (&tiles)[COUNT], int64_t M, int64_t N, int64_t Kp, bool split) {
-  const int64_t C = Kp / kChunk, cus = resident_slots() / 2;
+  const int C = static_cast<int>(Kp / kChunk), cus = resident_slots() / 2;
   GemmPlan best{0, 1};
   float least = -1.f;
   for (int t = 0; t < COUNT; ++t) {
     const TileCost& k = tiles[t];
+    const int64_t tiles_mn = ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn);
+    const int slots = cus * k.per_cu;
     for (int s = 1; s <= (split ? kMaxSlices : 1) && s * 2 <= C + 1; s *= 2) {
-      const int64_t wgs = ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn) * s;
-      const int64_t slots = cus * k.per_cu, rounds = wgs / slots;
+      const int64_t wgs = tiles_mn * s, rounds = wgs / slots;
       const float chunks = static_cast<float>((C + s - 1) / s);
       const float part = static_cast<float>(wgs - rounds * slots) / static_cast<float>(slots);
       float us = static_cast<float>(rounds) * (chunks * k.full + k.ends);
@@ -606,6 +607,10 @@ GemmPlan least(const TileCost (&tiles)[COUNT], int64_t M, int64_t N, int64_t Kp,
 
 GemmPlan gemm_plan(int64_t M, int64_t N, int64_t Kp, bool f32, bool split) {
   return f32 ? least(kTiles32, M, N, Kp, split) : least(kTiles16, M, N, Kp, split);
+}
+
+size_t split_bytes(int slices, int64_t M, int64_t N) {
+  return slices > 1 ? static_cast<size_t>(slices) * M * part_ld(N) * 4 : 0;
 }
 
 template <int YT, bool GELU>
@@ -625,12 +630,13 @@ void launch_tiles(const GemmArgs& g, hipStream_t stream) {
 }
 
 template <int YT, bool GELU>
-hipError_t launch_e(GemmArgs& g, hipStream_t stream) {
+hipError_t launch_e(GemmArgs& g, size_t part_bytes, hipStream_t stream) {
   if (g.M <= kFewRows) {
     launch_rows<YT, GELU>(g, stream);
     return hipGetLastError();
   }
-  const GemmPlan p = gemm_plan(g.M, g.N, g.Kp, YT == SVDQ_F32, g.part != nullptr);
+  GemmPlan p = gemm_plan(g.M, g.N, g.Kp, YT == SVDQ_F32, g.part != nullptr);
+  if (part_bytes < split_bytes(p.slices, g.M, g.N)) p = gemm_plan(g.M, g.N, g.Kp, YT == SVDQ_F32, false);
   g.slices = p.slices;
   if constexpr (YT == SVDQ_F32) {
     // operands widened to fp16 take twice the registers
@@ -657,20 +663,22 @@ size_t gemm_fp8_split_bytes(int64_t M, int64_t N, int64_t Kp) {
   if (M <= kFewRows) return 0;
   const int s16 = gemm_plan(M, N, Kp, false, true).slices;
   const int s32 = gemm_plan(M, N, Kp, true, true).slices;
-  const int s = s16 > s32 ? s16 : s32;
-  return s > 1 ? static_cast<size_t>(s) * M * part_ld(N) * 4 : 0;
+  return split_bytes(s16 > s32 ? s16 : s32, M, N);
 }
 
 hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
                            const float* w_scales, const float* bias, void* Y, int y_dtype,
                            int64_t M, int64_t N, int64_t Kp, int64_t ldy, bool gelu, float* part,
-                           hipStream_t stream) {
+                           size_t part_bytes, hipStream_t stream) {
   GemmArgs g{a_codes, w_codes, a_scales, w_scales, bias, Y, part, M, N, Kp, ldy, 1};
   if (y_dtype == SVDQ_F16)
-    return gelu ? launch_e<SVDQ_F16, true>(g, stream) : launch_e<SVDQ_F16, false>(g, stream);
+    return gelu ? launch_e<SVDQ_F16, true>(g, part_bytes, stream)
+                : launch_e<SVDQ_F16, false>(g, part_bytes, stream);
   if (y_dtype == SVDQ_BF16)
-    return gelu ? launch_e<SVDQ_BF16, true>(g, stream) : launch_e<SVDQ_BF16, false>(g, stream);
-  return gelu ? launch_e<SVDQ_F32, true>(g, stream) : launch_e<SVDQ_F32, false>(g, stream);
+    return gelu ? launch_e<SVDQ_BF16, true>(g, part_bytes, stream)
+                : launch_e<SVDQ_BF16, false>(g, part_bytes, stream);
+  return gelu ? launch_e<SVDQ_F32, true>(g, part_bytes, stream)
+                : launch_e<SVDQ_F32, false>(g, part_bytes, stream);
 }
 
 }  // namespace svdq
