@@ -23,8 +23,10 @@ from .api import (Conv2d, Linear, Prepared, attention, attention_workspace_bytes
                   quantize_act_lowrank_down_conv_mx, quantize_act_lowrank_down_conv_tiled,
                   quantize_act_lowrank_down_mx, smoothing_factors, w4a4_gemm_lowrank_up,
                   w4a16_gemm, w4a16_tile_activation, w4a16_x_tiled_bytes, linear_w4a16)
+from .block import AttentionBlock, KeyValueCache  # noqa: F401
 
-__all__ = ["Conv2d", "Linear", "Prepared", "attention", "attention_workspace_bytes",
+__all__ = ["AttentionBlock", "KeyValueCache",
+           "Conv2d", "Linear", "Prepared", "attention", "attention_workspace_bytes",
            "document_key_ranges", "fp8_padded", "gemm_fp8", "gemm_fp8_workspace_bytes",
            "linear_fp8", "linear_fp8_workspace_bytes", "prepare_weights_fp8",
            "quantize_act_fp8", "rmsnorm_quantize_fp8", "channel_absmax", "clock_mark", "clock_probe",

@@ -1,0 +1,52 @@
+"""The attention block's refusals, and its cache, without a GPU."""
+import numpy as np
+import pytest
+import torch
+
+import bit_post_quantized_smooth_amd as sq
+
+
+def weights(K=256, Hq=4, Hkv=2, D=32):
+    rng = np.random.default_rng(0)
+    f = lambda *s: rng.standard_normal(s).astype(np.float32)
+    return sq.prepare_weights_fp8(f(K, (Hq + 2 * Hkv) * D)), sq.prepare_weights_fp8(f(Hq * D, K))
+
+
+def test_weights_that_do_not_fit():
+    qkv, out = weights()
+    gain = np.ones(256, np.float32)
+    with pytest.raises(ValueError, match="do not fit"):
+        sq.AttentionBlock(gain, qkv, out, 4, 4, 32, device="cpu")
+    with pytest.raises(ValueError, match="do not fit"):
+        sq.AttentionBlock(gain, out, qkv, 4, 2, 32, device="cpu")
+    with pytest.raises(ValueError, match="prepare_weights_fp8"):
+        sq.AttentionBlock(gain, sq.prepare_weights(np.ones((256, 256), np.float32), np.ones(256, np.float32), 0),
+                          out, 4, 2, 32, device="cpu")
+
+
+def test_inputs_that_do_not_fit():
+    block = sq.AttentionBlock(np.ones(256, np.float32), *weights(), 4, 2, 32, device="cpu")
+    X = torch.zeros(2, 3, 256, dtype=torch.float16)
+    for bad, match in ((X[0], "shape"), (X[..., :128], "shape"), (X.float(), "dtype")):
+        with pytest.raises(ValueError, match=match):
+            block(bad)
+    with pytest.raises(TypeError):
+        block(X.numpy())
+    with pytest.raises(ValueError, match="residual"):
+        block(X, X[:1])
+    with pytest.raises(ValueError, match="dtype"):
+        block(X, X.bfloat16())
+    with pytest.raises(ValueError, match="on a GPU"):
+        block(X)
+
+
+def test_cache():
+    c = sq.KeyValueCache(2, 10, 3, 8, torch.float16, device="cpu")
+    a = torch.arange(2 * 4 * 3 * 8, dtype=torch.float16).view(2, 4, 3, 8)
+    k, v = c.append(a, -a)
+    assert torch.equal(k, a) and torch.equal(v, -a) and c.length == 4
+    k, v = c.append(a + 1, a)
+    assert k.shape[1] == 8 and torch.equal(k[:, 4:], a + 1) and torch.equal(v[:, :4], -a)
+    with pytest.raises(ValueError, match="cache of 10"):
+        c.append(a, a)
+    assert c.length == 8
