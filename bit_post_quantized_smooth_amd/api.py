@@ -968,6 +968,13 @@ def _ld(t) -> int:
     return t.stride()[0] if rows > 1 else cols or 1
 
 
+@functools.lru_cache(maxsize=None)
+def _block_types():
+    """fp32, the e4m3 types and the activation types, for the checks of whole calls
+    that come before the ones with a message for each tensor."""
+    return _torch().float32, _dtypes(_E4M3), _dtypes(_BLOCK_X)
+
+
 def _fp8_side(name, rows, Kp, codes, scales, srows):
     _buf(name + "_codes", codes, _E4M3, nbytes=rows * Kp)
     _buf(name + "_scales", scales, _F32, nbytes=4 * srows * (Kp // FP8_BLOCK))
@@ -979,20 +986,32 @@ def rmsnorm_quantize_fp8(X, residual, gain, eps: float, a_codes, a_scales, resid
     residual_out (may be None, or X or residual itself); the RMS norm of h times
     gain (may be None) as e4m3 codes (M x fp8_padded(K)) and fp32 scales (M x
     fp8_padded(K)/128)."""
-    _mat("X", X, None, None, _BLOCK_X)
-    shape, dtype = X.shape, X.dtype
-    M, K = shape
-    for name, t in (("residual", residual), ("residual_out", residual_out)):
-        if t is not None and not (t.__class__ is X.__class__ and t.dtype is dtype
-                                  and t.shape == shape and t.is_contiguous()):
-            _mat(name, t, M, K, _BLOCK_X)
-            if t.dtype != dtype:
-                raise ValueError(f"{name}: dtype {t.dtype}, X has {dtype}")
+    f32, e4m3, block_x = _block_types()
+    try:
+        shape, dtype = X.shape, X.dtype
+        M, K = shape
+        Kp = -(-K // FP8_BLOCK) * FP8_BLOCK
+        good = (dtype in block_x and X.is_contiguous()
+                and (residual is None or residual.dtype is dtype and residual.shape == shape
+                     and residual.is_contiguous())
+                and (residual_out is None or residual_out.dtype is dtype
+                     and residual_out.shape == shape and residual_out.is_contiguous())
+                and a_codes.dtype in e4m3 and a_codes.nbytes == M * Kp and a_codes.is_contiguous()
+                and a_scales.dtype is f32 and a_scales.nbytes == M * Kp // (FP8_BLOCK // 4)
+                and a_scales.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _mat("X", X, None, None, _BLOCK_X)
+        M, K = X.shape
+        for name, t in (("residual", residual), ("residual_out", residual_out)):
+            if t is not None:
+                _mat(name, t, M, K, _BLOCK_X)
+                if t.dtype != X.dtype:
+                    raise ValueError(f"{name}: dtype {t.dtype}, X has {X.dtype}")
+        _fp8_side("a", M, fp8_padded(K), a_codes, a_scales, M)
     if gain is not None:
         _buf("gain", gain, _F32, nbytes=4 * K)
-    Kp = -(-K // FP8_BLOCK) * FP8_BLOCK
-    _buf("a_codes", a_codes, _E4M3, nbytes=M * Kp)
-    _buf("a_scales", a_scales, _F32, nbytes=M * Kp // (FP8_BLOCK // 4))
     _on_gpu(X, residual, residual_out, gain, a_codes, a_scales)
     status = lib.svdq_rmsnorm_quantize_fp8(
         X.data_ptr(), None if residual is None else residual.data_ptr(), _dt_block(X), M, K,
@@ -1023,14 +1042,29 @@ def gemm_fp8(a_codes, a_scales, w_codes, w_scales, bias, Y, ws=None, stream=None
     """svdq_gemm_fp8: Y (M x N) from e4m3 codes a (M x Kp) and w (N x Kp) and their
     scales (M x Kp/128 and ceil(N/128) x Kp/128). With a workspace of
     gemm_fp8_workspace_bytes a shape of few tiles and long K is split along K."""
-    _mat("Y", Y, None, None, _BLOCK_X)
-    M, N = Y.shape
-    _mat("a_codes", a_codes, M, None, _E4M3)
-    Kp = a_codes.shape[1]
-    if Kp < FP8_BLOCK or Kp % FP8_BLOCK:
-        raise ValueError(f"a_codes: {Kp} columns, need a positive multiple of {FP8_BLOCK}")
-    _fp8_side("a", M, Kp, a_codes, a_scales, M)
-    _fp8_side("w", N, Kp, w_codes, w_scales, -(-N // FP8_BLOCK))
+    f32, e4m3, block_x = _block_types()
+    try:
+        M, N = Y.shape
+        m, Kp = a_codes.shape
+        G = Kp // FP8_BLOCK
+        good = (m == M and Kp == G * FP8_BLOCK > 0 and Y.dtype in block_x and Y.is_contiguous()
+                and a_codes.dtype in e4m3 and a_codes.is_contiguous()
+                and a_scales.dtype is f32 and a_scales.nbytes == 4 * M * G
+                and a_scales.is_contiguous() and w_codes.dtype in e4m3
+                and w_codes.nbytes == N * Kp and w_codes.is_contiguous()
+                and w_scales.dtype is f32 and w_scales.nbytes == -(-N // FP8_BLOCK) * 4 * G
+                and w_scales.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _mat("Y", Y, None, None, _BLOCK_X)
+        M, N = Y.shape
+        _mat("a_codes", a_codes, M, None, _E4M3)
+        Kp = a_codes.shape[1]
+        if Kp < FP8_BLOCK or Kp % FP8_BLOCK:
+            raise ValueError(f"a_codes: {Kp} columns, need a positive multiple of {FP8_BLOCK}")
+        _fp8_side("a", M, Kp, a_codes, a_scales, M)
+        _fp8_side("w", N, Kp, w_codes, w_scales, -(-N // FP8_BLOCK))
     _bias(bias, N)
     if ws is not None:
         _buf("ws", ws, _BYTES + _HALF + _F32)
