@@ -119,6 +119,12 @@ __device__ __forceinline__ v4f bias4(const GemmArgs& g, int64_t n) {
   return b;
 }
 
+template <int YT>
+__device__ __forceinline__ uint16_t bits16(float x) {
+  if constexpr (YT == SVDQ_F16) return f2h(x);
+  else return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+}
+
 // The bias, the optional GELU and the one rounding to a 16-bit output.
 template <int YT, bool GELU>
 __device__ __forceinline__ uint2 round4(v4f v, v4f b) {
@@ -127,8 +133,7 @@ __device__ __forceinline__ uint2 round4(v4f v, v4f b) {
   for (int e = 0; e < 4; ++e) {
     float x = v[e] + b[e];
     if constexpr (GELU) x = gelu_tanh_f32(x);
-    if constexpr (YT == SVDQ_F16) h[e] = f2h(x);
-    else h[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+    h[e] = bits16<YT>(x);
   }
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
@@ -441,13 +446,42 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
       return;
     }
   }
-  if (g.slices == 1) {
+  constexpr int ES = YT == SVDQ_F32 ? 4 : 2;
+  const bool vec = ((reinterpret_cast<uintptr_t>(g.Y) | (g.ldy * ES)) & (4 * ES - 1)) == 0;
+  if (g.slices == 1 && vec) {
 #pragma unroll
     for (int j = 0; j < NBN; ++j) {
       const v4f b = bias4(g, nw + 16 * j);
 #pragma unroll
       for (int i = 0; i < NBM; ++i)
         finish4<YT, GELU>(g, acc[i][j], b, mw + 16 * i + rl, nw + 16 * j);
+    }
+  } else if (g.slices == 1) {
+    // Rows that start at any address: single elements, but a wave's in the order
+    // they lie in, 16 rows at a time through its share of LDS. From the
+    // accumulators each store would reach 16 rows (2500 x 5127 x 2560: 60 us
+    // against 50).
+    constexpr int COLS = 16 * NBN, PITCH = COLS + 4;
+    static_assert(sizeof(lds) >= static_cast<size_t>(T::NW) * 16 * PITCH * 4, "room for 16 rows");
+    float* mem = reinterpret_cast<float*>(&lds) + wave * 16 * PITCH;
+    const int cols = static_cast<int>(g.N - nw0 < COLS ? g.N - nw0 : COLS);
+#pragma unroll
+    for (int i = 0; i < NBM; ++i) {
+#pragma unroll
+      for (int j = 0; j < NBN; ++j)
+        *reinterpret_cast<v4f*>(mem + rl * PITCH + 16 * j + 4 * q) =
+            acc[i][j] + bias4(g, nw + 16 * j);
+#pragma unroll
+      for (int t = 0; t < 4 * NBN; ++t) {
+        const int at = 64 * t + lane, row = at / COLS, col = at % COLS;
+        const int64_t m = mw + 16 * i + row;
+        if (m < g.M && col < cols) {
+          float x = mem[row * PITCH + col];
+          if constexpr (GELU) x = gelu_tanh_f32(x);
+          if constexpr (YT == SVDQ_F32) static_cast<float*>(g.Y)[m * g.ldy + nw0 + col] = x;
+          else static_cast<uint16_t*>(g.Y)[m * g.ldy + nw0 + col] = bits16<YT>(x);
+        }
+      }
     }
   } else {
 #pragma unroll
