@@ -769,47 +769,53 @@ hipError_t launch_t(const AttnArgs& g, const AttnPlan& p, hipStream_t stream) {
 
 }  // namespace
 
-// The split along the keys of least estimated time, in microseconds measured at
-// D = 128: a tile of a workgroup that has its compute unit to itself takes 1.8
-// (128 keys, few rows) or 1.2 (64 keys, 128 rows); few rows are bound by memory
-// from about 150 workgroups on, 128 rows share their unit beyond one workgroup
-// each; a workgroup's start and end take 2.5, and joining splits 4 and their
-// outputs written and read at 4 TB/s. One token, 32 heads over 8, 8 caches of 8191:
-// 55 us with 4 splits, 124 with one, 65 with 16; one cache: 17, 78 (32 splits).
+// The row tile (128 rows, a wave each 32 of them, or 32, the waves sharing a
+// tile's keys) and the split along the keys of least estimated time, in
+// microseconds measured at D = 128: a tile of a workgroup that has its compute
+// unit to itself takes 1.8 (128 keys, 32 rows) or 1.2 (64 keys, 128 rows); 32 rows
+// are bound by memory from about 150 workgroups on, 128 rows share their unit
+// beyond one workgroup each; a workgroup's start and end take 2.5, and joining
+// splits 6 and their outputs written and read at 4 TB/s. One token, 32 heads over
+// 8, 8 caches of 8191: 55 us with 4 splits, 124 with one, 65 with 16; one cache: 17,
+// 78 (32 splits). 32 rows against 128: 500 causal tokens of 8 heads 9.4 against
+// 16.8 us, 1000 of 4 heads 17 against 23, 77 of 24 heads alike.
 AttnPlan attention_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D,
                         bool split) {
   AttnPlan p{};
   const int64_t rows = Lq * (Hq / Hkv);
-  p.few = rows <= 32;
-  p.row_tiles = (rows + (p.few ? 31 : 127)) / (p.few ? 32 : 128);
-  const int64_t wgs = p.row_tiles * B * Hkv;
-  const int64_t tiles = (Lk + (p.few ? 127 : 63)) / (p.few ? 128 : 64);
   const int cus = resident_slots() / 2;
-  const int slots = p.few && D > 64 ? cus : 2 * cus;
   float least = -1.f;
-  p.splits = 1;
   constexpr int kTried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
-  for (const int s : kTried) {
-    if (!split || s > kMaxSplits || (s > 1 && s > tiles)) break;
-    const float all = static_cast<float>(wgs) * static_cast<float>(s);
-    const float active = all < slots ? all : static_cast<float>(slots);
-    const float rounds = std::ceil(all / static_cast<float>(slots));
-    float tile;
-    if (p.few) {
-      tile = 0.0124f * active * (D > 64 ? 1.f : 0.5f);
-      if (tile < 1.8f) tile = 1.8f;
-    } else {
-      tile = active <= cus ? 1.2f : 1.2f + 1.3f * (active - cus) / cus;
-    }
-    float us = rounds * (static_cast<float>((tiles + s - 1) / s) * tile + 2.5f);
-    if (s > 1)
-      us += 4.f + static_cast<float>(B * Lq) * static_cast<float>(Hq * D) * s * 8.f / 4e6f;
-    if (least < 0.f || us < least) {
-      least = us;
-      p.splits = s;
+  for (const bool few : {true, false}) {
+    if (!few && rows <= 32) break;
+    const int64_t row_tiles = (rows + (few ? 31 : 127)) / (few ? 32 : 128);
+    const int64_t wgs = row_tiles * B * Hkv;
+    const int64_t tiles = (Lk + (few ? 127 : 63)) / (few ? 128 : 64);
+    const int slots = few && D > 64 ? cus : 2 * cus;
+    for (const int s : kTried) {
+      if (s > 1 && (!split || s > kMaxSplits || s > tiles)) break;
+      const float all = static_cast<float>(wgs) * static_cast<float>(s);
+      const float active = all < slots ? all : static_cast<float>(slots);
+      const float rounds = std::ceil(all / static_cast<float>(slots));
+      float tile;
+      if (few) {
+        tile = 0.0124f * active * (D > 64 ? 1.f : 0.5f);
+        if (tile < 1.8f) tile = 1.8f;
+      } else {
+        tile = active <= cus ? 1.2f : 1.2f + 1.3f * (active - cus) / cus;
+      }
+      float us = rounds * (static_cast<float>((tiles + s - 1) / s) * tile + 2.5f);
+      if (s > 1)
+        us += 6.f + static_cast<float>(B * Lq) * static_cast<float>(Hq * D) * s * 8.f / 4e6f;
+      if (least < 0.f || us < least) {
+        least = us;
+        p.few = few;
+        p.row_tiles = row_tiles;
+        p.wgs = wgs * s;
+        p.splits = s;
+      }
     }
   }
-  p.wgs = wgs * p.splits;
   p.grid = static_cast<unsigned>(p.wgs);
   return p;
 }

@@ -31,7 +31,7 @@ struct AttnArgs {
 };
 
 struct AttnPlan {
-  bool few;                  // at most 32 rows per key head: waves split the keys
+  bool few;                  // row tiles of 32 rows: the waves split a tile's keys
   int64_t row_tiles, wgs;
   int splits;                // workgroups along the keys
   unsigned grid;
