@@ -27,10 +27,28 @@
 //
 // K and V go from global memory straight into LDS (two stages), rows of DP
 // channels with their 16-byte units XOR-swizzled by the row; channels past D
-// and keys outside the tile read as zero. Work is split along the keys where
-// there are few rows: over the workgroup's waves (KW = 4) and over workgroups,
-// which then write fp32 outputs with their maxima and sums for a second kernel
-// that joins them in order.
+// and keys outside the tile read as zero. A workgroup takes 128 rows (RW = 4: a
+// wave each 32, all sharing the tiles of 64 keys) or 32 (RW = 1: the waves share
+// out tiles of 128 keys and add their outputs at the end), and work may be split
+// along the keys over workgroups, which then write fp32 outputs with their maxima
+// and sums for a second kernel that joins them in order.
+//
+// The maximum that the exponents refer to is raised only when a score exceeds it
+// by 2^8 (kGrow): the outputs are then rescaled, otherwise they stay in place. The
+// products of one half of a tile go out beside the exponents of the other. Tiles
+// that no row sees in part run a loop without masks; tiles cut by a mask, and a
+// wave's tiles of which it sees nothing, have loops of their own, since a branch
+// inside one loop moves the outputs between registers. V of a hidden key times a
+// weight of 0 is NaN where V is not finite: only if an output comes out so is the
+// pass repeated with hidden keys' V taken out.
+//
+// Measured (D = 128). 24 heads of 4608 x 4608, fp16: 288 to 312 us by box, 840 to
+// 900 TFLOP/s; the matrix core is busy 42% of the time, beside 6.5 vector
+// instructions per matrix instruction, and 864 workgroups are 1.69 rounds of the
+// 512 that fit. Packed documents of the same length: 135 us. 16 heads over 4, 8191
+// causal rows with a prefix and capped scores, bf16: 360 to 415 us, the cap's
+// exponential and reciprocal doubling the vector work per score. One token, 32
+// heads over 8, 8 caches of 8191: 42 us plus 5 us to join, 210 MB at 5.0 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -47,7 +65,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kWaves = 4;
-constexpr float kGrow = 8.f;
+constexpr float kGrow = 8.f;         // how far scores may exceed the reference, base 2
 constexpr float kLarge = 1e6f;       // logits (base 2); their rounding is below 2^-4
 
 template <class T>

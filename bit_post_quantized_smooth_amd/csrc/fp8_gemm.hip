@@ -22,11 +22,23 @@
 // - tiles: a workgroup computes BM x BN outputs, both operands copied from
 //   global memory straight into LDS, one 128-byte row piece per row and chunk,
 //   its 16-byte units XOR-swizzled so that the operand reads of 16 lanes cover
-//   all banks. Optionally split along K, each slice writing fp32 partial tiles.
+//   all banks. From 256 x 256 (the fewest bytes read again per product) to 64 x
+//   64 (the most workgroups), chosen by estimated time; optionally split along K,
+//   each slice writing fp32 partial tiles.
 // - few rows (M <= 16): bound by reading the weights once. A workgroup owns 16
 //   columns, its waves take the groups in turn, operands go straight to
 //   registers, and the waves' accumulators are added through LDS in order.
 // - the sums of a product split along K, in slice order.
+//
+// Measured. 4608 x 9216 x 3072 to fp16: 136 to 147 us by box, 1.8 to 1.9 PFLOP/s;
+// the matrix core is busy 42% of the time, the clock falls to 1.9 GHz under it, and
+// 648 tiles are 2.53 rounds of the 256 compute units. A chunk of a 256 x 256 tile
+// takes 1.55 us, which is the rate of a large library product without group
+// scales; what is lost is the last round and 7 us of start and end per tile. One
+// row, 10240 x 1280: 4.8 us for 13 MB. 24 x 3072 x 12288: 10.7 us the tiles of 16
+// slices (3.5 TB/s) and 3 us their sums. 1023 x 1283 x 1272 to fp32: 15 us, of which
+// 7 are a launch, a tile's start and its end, the rest 10 chunks of 0.65 us that
+// wait for their copies and LDS reads (without the widening 0.55).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
