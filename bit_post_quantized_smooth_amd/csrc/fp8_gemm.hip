@@ -121,6 +121,9 @@ __device__ __forceinline__ v4f mfma_group(const Frag<true>& w, const Frag<true>&
   return p;
 }
 
+// Global vectors may lie at any address that their elements may.
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // The 4 bias values of columns n .. n+3 (0 without a bias and past the end).
 __device__ __forceinline__ v4f bias4(const GemmArgs& g, int64_t n) {
   v4f b = v4f{0.f, 0.f, 0.f, 0.f};
@@ -431,20 +434,23 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
   const int64_t mw = m0 + wm * NBM * 16, nw = nw0 + 4 * q;
   // A 16-bit Y goes out through the wave's share of LDS, from where a
   // lane stores 16 bytes and its neighbours the rest of the row's columns,
-  // instead of 4 lanes a 32-byte piece of it. Rows of 32 * NBN bytes, padded by
-  // 16 to spread the banks.
+  // instead of 4 lanes a 32-byte piece of it, at any address (one that is not
+  // aligned costs less than single elements: 8000 x 3001 x 128 28 us against 36).
+  // Rows of 32 * NBN bytes, padded by 16 to spread the banks.
+  constexpr int COLS = 16 * NBN, PITCH = COLS + 4;    // the fp32 rows further below
+  constexpr int RB = 32 * NBN + 16, UN = 2 * NBN;     // bytes and 16-byte units of a row
+  constexpr int SHARE = YT == SVDQ_F32 ? 16 * PITCH * 4 : NBM * 16 * RB;   // a wave's bytes
+  static_assert(SHARE >= 16 * PITCH * 4 && sizeof(lds) >= static_cast<size_t>(T::NW) * SHARE,
+                "a share holds what either way of storing puts there");
+  uint8_t* share = reinterpret_cast<uint8_t*>(&lds) + wave * SHARE;
   if constexpr (YT != SVDQ_F32) {
-    constexpr int RB = 32 * NBN + 16, UN = 2 * NBN;   // bytes and 16-byte units of a row
-    static_assert(sizeof(lds) >= static_cast<size_t>(T::NW) * NBM * 16 * RB, "room for the tile");
-    if (g.slices == 1 && nw0 + NBN * 16 <= g.N &&
-        ((reinterpret_cast<uintptr_t>(g.Y) | (g.ldy * 2)) & 15) == 0) {
-      uint8_t* mem = reinterpret_cast<uint8_t*>(&lds) + wave * NBM * 16 * RB;
+    if (g.slices == 1 && nw0 + NBN * 16 <= g.N) {
 #pragma unroll
       for (int j = 0; j < NBN; ++j) {
         const v4f b = bias4(g, nw + 16 * j);
 #pragma unroll
         for (int i = 0; i < NBM; ++i)
-          *reinterpret_cast<uint2*>(mem + (16 * i + rl) * RB + 32 * j + 8 * q) =
+          *reinterpret_cast<uint2*>(share + (16 * i + rl) * RB + 32 * j + 8 * q) =
               round4<YT, GELU>(acc[i][j], b);
       }
       uint16_t* y = static_cast<uint16_t*>(g.Y) + mw * g.ldy + nw0;
@@ -452,8 +458,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
 #pragma unroll
       for (int t = 0; t < NBM * 16 * UN / 64; ++t) {
         const int at = 64 * t + lane, row = at / UN, col = at % UN;
-        const v4i v = *reinterpret_cast<const v4i*>(mem + row * RB + 16 * col);
-        if (row < rows) *reinterpret_cast<v4i*>(y + row * g.ldy + 8 * col) = v;
+        const v4i v = *reinterpret_cast<const v4i*>(share + row * RB + 16 * col);
+        if (row < rows) *reinterpret_cast<v4i_any*>(y + row * g.ldy + 8 * col) = v;
       }
       return;
     }
@@ -469,13 +475,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tiles(const GemmArgs g,
         finish4<YT, GELU>(g, acc[i][j], b, mw + 16 * i + rl, nw + 16 * j);
     }
   } else if (g.slices == 1) {
-    // Rows that start at any address: single elements, but a wave's in the order
-    // they lie in, 16 rows at a time through its share of LDS. From the
-    // accumulators each store would reach 16 rows (2500 x 5127 x 2560: 60 us
-    // against 50).
-    constexpr int COLS = 16 * NBN, PITCH = COLS + 4;
-    static_assert(sizeof(lds) >= static_cast<size_t>(T::NW) * 16 * PITCH * 4, "room for 16 rows");
-    float* mem = reinterpret_cast<float*>(&lds) + wave * 16 * PITCH;
+    // fp32 rows at any address, and 16-bit ones that end inside the wave's columns:
+    // single elements, but in the order they lie in, 16 rows at a time through the
+    // wave's share of LDS. From the accumulators each store would reach 16 rows
+    // (fp32 2500 x 2501 x 2560: 57 us against 49).
+    float* mem = reinterpret_cast<float*>(share);
     const int cols = static_cast<int>(g.N - nw0 < COLS ? g.N - nw0 : COLS);
 #pragma unroll
     for (int i = 0; i < NBM; ++i) {
