@@ -42,7 +42,7 @@
 // weight of 0 is NaN where V is not finite: only if an output comes out so is the
 // pass repeated with hidden keys' V taken out.
 //
-// Measured (D = 128). 24 heads of 4608 x 4608, fp16: 288 to 312 us by box, 840 to
+// Measured (D = 128). 24 heads of 4608 x 4608, fp16: 288 to 312 us by card, 840 to
 // 900 TFLOP/s; the matrix core is busy 42% of the time, beside 6.5 vector
 // instructions per matrix instruction, and 864 workgroups are 1.69 rounds of the
 // 512 that fit. Packed documents of the same length: 135 us. 16 heads over 4, 8191

@@ -30,7 +30,7 @@
 //   registers, and the waves' accumulators are added through LDS in order.
 // - the sums of a product split along K, in slice order.
 //
-// Measured. 4608 x 9216 x 3072 to fp16: 136 to 147 us by box, 1.8 to 1.9 PFLOP/s;
+// Measured. 4608 x 9216 x 3072 to fp16: 136 to 147 us by card, 1.8 to 1.9 PFLOP/s;
 // the matrix core is busy 42% of the time, the clock falls to 1.9 GHz under it, and
 // 648 tiles are 2.53 rounds of the 256 compute units. A chunk of a 256 x 256 tile
 // takes 1.55 us, which is the rate of a large library product without group
