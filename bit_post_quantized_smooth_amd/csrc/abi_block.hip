@@ -83,7 +83,8 @@ int check_gemm(const char* fn, const uint8_t* a_codes, const float* a_scales,
   if (Kp < SVDQ_FP8_BLOCK || Kp % SVDQ_FP8_BLOCK != 0)
     return fail(SVDQ_ERR_GROUP, fn, "Kp is not a positive multiple of 128");
   if (Kp > kMaxK || M < 0 || M > kMaxRows || N < 1 || N > kMaxRows || ldy < N ||
-      ldy > kMaxStride || ((M + 63) / 64) * ((N + 63) / 64) > (int64_t{1} << 26)) {
+      ldy > kMaxStride || ((M + 63) / 64) * ((N + 63) / 64) > (int64_t{1} << 26) ||
+      !gemm_fp8_fits(M, N, y_dtype)) {
     set_error("%s: M=%lld N=%lld Kp=%lld ldy=%lld out of range", fn, (long long)M, (long long)N,
               (long long)Kp, (long long)ldy);
     return SVDQ_ERR_SHAPE;
@@ -274,16 +275,16 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
   if (sk[1] > kMaxK || sv[1] > kMaxK || (Lk > 1 && (sk[1] < D || sv[1] < D)))
     return fail(SVDQ_ERR_SHAPE, fn, "token strides of K and V must lie in D .. 2^22");
   if (B == 0 || Lq == 0) return SVDQ_OK;
+  AttnPlan p = attention_plan(B, Lq, Lk, Hq, Hkv, D, true);
+  if (p.grid == 0) return fail(SVDQ_ERR_SHAPE, fn, "more rows than one launch can cover");
   if (!Q || !Out || (Lk > 0 && (!K || !V))) return fail(SVDQ_ERR_NULL, fn, "null pointer");
   if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(Out, 16) ||
       !aligned(slopes, 4) || !aligned(prefix, 4) || !aligned(key_ranges, 4) || !aligned(ws, 16))
     return fail(SVDQ_ERR_ALIGN, fn,
                 "Q, K, V, Out and the workspace must be 16-byte aligned, the rest 4-byte");
   if (int s = device_ready(fn)) return s;
-  AttnPlan p = attention_plan(B, Lq, Lk, Hq, Hkv, D, true);
   if (p.splits > 1 && (ws == nullptr || ws_bytes < attention_bytes(B, Lq, Hq, D, p.splits)))
     p = attention_plan(B, Lq, Lk, Hq, Hkv, D, false);
-  if (p.wgs > kMaxRows) return fail(SVDQ_ERR_SHAPE, fn, "too many rows");
   AttnArgs g{};
   g.q = Q;
   g.k = K;

@@ -56,6 +56,7 @@
 #include "../../include/svdq.h"
 #include "attention.hpp"
 #include "block_common.hpp"
+#include "block_launch.hpp"
 #include "k2_common.hpp"
 
 namespace svdq {
@@ -803,7 +804,7 @@ AttnPlan attention_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t H
   const int64_t rows = Lq * (Hq / Hkv);
   const int cus = resident_slots() / 2;
   float least = -1.f;
-  constexpr int kTried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+  constexpr int kTried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, kMaxSplits};
   for (const bool few : {true, false}) {
     if (!few && rows <= 32) break;
     const int64_t row_tiles = (rows + (few ? 31 : 127)) / (few ? 32 : 128);
@@ -811,7 +812,10 @@ AttnPlan attention_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t H
     const int64_t tiles = (Lk + (few ? 127 : 63)) / (few ? 128 : 64);
     const int slots = few && D > 64 ? cus : 2 * cus;
     for (const int s : kTried) {
-      if (s > 1 && (!split || s > kMaxSplits || s > tiles)) break;
+      if (s > 1 && (!split || s > tiles)) break;
+      // the grids of the kernel and of the join of its rows
+      if (!grid_fits(wgs * s, 64 * kWaves) || (s > 1 && !grid_fits(B * Hkv * rows, 32 * kJoin)))
+        break;
       const float all = static_cast<float>(wgs) * static_cast<float>(s);
       const float active = all < slots ? all : static_cast<float>(slots);
       const float rounds = std::ceil(all / static_cast<float>(slots));

@@ -37,6 +37,7 @@ struct AttnPlan {
   unsigned grid;
 };
 
+// grid 0: no row tile's grid can cover the rows.
 AttnPlan attention_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D,
                         bool split);
 hipError_t launch_attention(AttnArgs g, int dtype, const AttnPlan& p, hipStream_t stream);

@@ -10,6 +10,10 @@ namespace svdq {
 
 constexpr int kFp8Block = 128;      // channels per e4m3 scale
 
+// A launch takes fewer than 2^32 threads: more are not refused, their number is cut
+// to 32 bits and the rest of the grid never runs.
+inline bool grid_fits(int64_t wgs, int threads) { return wgs <= 0xFFFFFFFFll / threads; }
+
 inline int64_t fp8_padded(int64_t K) { return (K + kFp8Block - 1) / kFp8Block * kFp8Block; }
 
 // norm: the RMS norm (gain may be null, eps); else the rows are quantized as
@@ -28,5 +32,7 @@ hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const 
                            int64_t M, int64_t N, int64_t Kp, int64_t ldy, bool gelu, float* part,
                            size_t part_bytes, hipStream_t stream);
 size_t gemm_fp8_split_bytes(int64_t M, int64_t N, int64_t Kp);
+// Whether a kernel's grid can cover M x N.
+bool gemm_fp8_fits(int64_t M, int64_t N, int y_dtype);
 
 }  // namespace svdq

@@ -609,17 +609,17 @@ constexpr int kFewRows = 16;
 // chunk when a workgroup has the chip almost to itself and when every slot is
 // taken, and of a tile's start and end.
 struct TileCost {
-  int bm, bn, per_cu;
+  int bm, bn, threads, per_cu;
   float alone, full, ends;
 };
-constexpr TileCost kTiles16[] = {{256, 256, 1, 1.25f, 1.55f, 7.0f},
-                                 {256, 192, 1, 1.06f, 1.35f, 6.0f},
-                                 {128, 128, 2, 0.77f, 1.00f, 4.0f},
-                                 {64, 128, 3, 0.60f, 0.95f, 4.0f},
-                                 {64, 64, 2, 0.24f, 0.40f, 2.5f}};
-constexpr TileCost kTiles32[] = {{256, 128, 1, 1.60f, 2.10f, 6.0f},
-                                 {64, 128, 3, 0.90f, 1.65f, 4.0f},
-                                 {64, 64, 2, 0.50f, 0.72f, 2.5f}};
+constexpr TileCost kTiles16[] = {{256, 256, 512, 1, 1.25f, 1.55f, 7.0f},
+                                 {256, 192, 512, 1, 1.06f, 1.35f, 6.0f},
+                                 {128, 128, 256, 2, 0.77f, 1.00f, 4.0f},
+                                 {64, 128, 256, 3, 0.60f, 0.95f, 4.0f},
+                                 {64, 64, 256, 2, 0.24f, 0.40f, 2.5f}};
+constexpr TileCost kTiles32[] = {{256, 128, 512, 1, 1.60f, 2.10f, 6.0f},
+                                 {64, 128, 256, 3, 0.90f, 1.65f, 4.0f},
+                                 {64, 64, 256, 2, 0.50f, 0.72f, 2.5f}};
 
 struct GemmPlan {
   int tile, slices;
@@ -641,6 +641,7 @@ GemmPlan least(const TileCost (&tiles)[COUNT], int64_t M, int64_t N, int64_t Kp,
     const int slots = cus * k.per_cu;
     for (int s = 1; s <= (split ? kMaxSlices : 1) && s * 2 <= C + 1; s *= 2) {
       const int64_t wgs = tiles_mn * s, rounds = wgs / slots;
+      if (!grid_fits(wgs, k.threads)) break;
       const float chunks = static_cast<float>((C + s - 1) / s);
       const float part = static_cast<float>(wgs - rounds * slots) / static_cast<float>(slots);
       float us = static_cast<float>(rounds) * (chunks * k.full + k.ends);
@@ -714,6 +715,13 @@ size_t gemm_fp8_split_bytes(int64_t M, int64_t N, int64_t Kp) {
   const int s16 = gemm_plan(M, N, Kp, false, true).slices;
   const int s32 = gemm_plan(M, N, Kp, true, true).slices;
   return split_bytes(s16 > s32 ? s16 : s32, M, N);
+}
+
+bool gemm_fp8_fits(int64_t M, int64_t N, int y_dtype) {
+  if (M <= kFewRows) return grid_fits((N + 15) / 16, 64 * kRowWaves);
+  const TileCost& largest = y_dtype == SVDQ_F32 ? kTiles32[0] : kTiles16[0];
+  return grid_fits(((M + largest.bm - 1) / largest.bm) * ((N + largest.bn - 1) / largest.bn),
+                   largest.threads);
 }
 
 hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,

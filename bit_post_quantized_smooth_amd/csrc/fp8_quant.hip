@@ -257,9 +257,20 @@ __global__ __launch_bounds__(256) void quantize_fp8_kernel(const QuantArgs q) {
 template <class T, bool NORM>
 void launch_t(const QuantArgs& q, hipStream_t stream) {
   const int64_t per_wave = 64 * VEC, per_wg = 256 * VEC;
+  // as many launches as the rows need, each of a grid that fits
+  constexpr int64_t kMaxWgs = 0xFFFFFFFFll / 256;
   auto go = [&](auto kernel, int rows) {
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((q.M + rows - 1) / rows)), dim3(256), 0,
-                       stream, q);
+    QuantArgs p = q;
+    for (int64_t at = 0; at < q.M; at += kMaxWgs * rows) {
+      p.X = static_cast<const T*>(q.X) + at * q.ldx;
+      if (q.residual) p.residual = static_cast<const T*>(q.residual) + at * q.ldr;
+      if (q.residual_out) p.residual_out = static_cast<T*>(q.residual_out) + at * q.ldo;
+      p.codes = q.codes + at * q.Kp;
+      p.scales = q.scales + at * (q.Kp / kFp8Block);
+      p.M = q.M - at < kMaxWgs * rows ? q.M - at : kMaxWgs * rows;
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((p.M + rows - 1) / rows)), dim3(256),
+                         0, stream, p);
+    }
   };
   if (q.K < VEC) go(quantize_fp8_kernel<T, NORM, 256, 0>, 1);
   else if (q.Kp <= per_wave) go(quantize_fp8_kernel<T, NORM, 64, 1>, 4);

@@ -669,7 +669,11 @@ int svdq_gelu_tanh_f16(const uint16_t* x, uint16_t* y, int64_t n, hipStream_t st
  *
  * Rows are row-major with unit inner stride and any row stride; X, residual and
  * residual_out need only the alignment of their element type. M = 0 (and for
- * attention B or Lq = 0) is a call that does nothing.
+ * attention B or Lq = 0) is a call that does nothing. A launch covers fewer than
+ * 2^32 threads: the product refuses (SVDQ_ERR_SHAPE) outputs of 2^23 or more tiles of
+ * 256 x 256 (256 x 128 in f32), or of 2^27 or more columns in up to 16 rows, and the
+ * attention 2^24 or more workgroups, which take up to 128 rows (query and query head)
+ * of one key head each.
  */
 
 /* Host: W (K x N row-major fp32, Y = X . W) -> w_codes, w_scales. */
