@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "../../include/svdq.h"
 #include "attention.hpp"
@@ -304,8 +305,11 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
   constexpr float kLog2e = 1.4426950408889634f;
   g.q_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
   g.scale2 = g.q_sign != 0 ? std::fabs(scale) * kLog2e : 1.f;
-  g.cap_in = softcap > 0.f ? 2.0f * kLog2e * (std::fabs(scale) / softcap) : 0.f;
-  g.cap2 = softcap * kLog2e;
+  // finite at any cap: a score of 0 times an infinity would be NaN
+  constexpr float kMost = std::numeric_limits<float>::max();
+  g.cap = softcap == 0.f ? kNoCap : softcap <= kNearest ? kNearCap : kAnyCap;
+  g.cap_in = softcap > 0.f ? std::fmin(2.0f * kLog2e * (std::fabs(scale) / softcap), kMost) : 0.f;
+  g.cap2 = std::fmin(softcap * kLog2e, kMost);
   g.B = static_cast<int>(B);
   g.Lq = static_cast<int>(Lq);
   g.Lk = static_cast<int>(Lk);

@@ -7,6 +7,10 @@
 
 namespace svdq {
 
+// Caps of the scores: none; up to kNearest, whose tanh may be off by 2^-23 of 1; any.
+enum { kNoCap = 0, kNearCap = 1, kAnyCap = 2 };
+constexpr float kNearest = 64.f;
+
 // Strides in elements: _b batch, _l token, _h head; channels are contiguous.
 struct AttnArgs {
   const void* q;
@@ -23,7 +27,8 @@ struct AttnArgs {
   // the kernel's scale is positive: its sign, or 0, goes into Q
   int q_sign;
   float scale2;              // |scale| * log2(e), 1 for a scale of 0
-  float cap_in, cap2;        // 2 log2(e) |scale| / cap, cap * log2(e); cap2 0: no cap
+  int cap;                   // kNoCap, kNearCap or kAnyCap
+  float cap_in, cap2;        // 2 log2(e) |scale| / cap, cap * log2(e)
   int B, Lq, Lk, Hkv, G, D;  // G query heads per key head
   int rows;                  // Lq * G
   int causal;

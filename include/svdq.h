@@ -728,7 +728,8 @@ size_t svdq_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t
                                       int64_t D);
 
 /* Device: masked attention with grouped heads.
- *   x[i][j] = scale * q_i . k_j; with softcap > 0: x = softcap * tanh(x / softcap);
+ *   x[i][j] = scale * q_i . k_j; with softcap > 0: x = softcap * tanh(x / softcap),
+ *   to 2^-19 of itself (softcap up to 64: or to 2^-21 of softcap);
  *   with slopes: x -= slopes[h] * |pos_i - j|, pos_i = i + Lk - Lq;
  *   out_i = sum_j softmax_j(x[i][j]) v_j over the keys j that row i sees:
  *   key_ranges (NULL, or [begin, end) int32 pairs per batch entry and query;

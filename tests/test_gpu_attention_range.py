@@ -1,0 +1,82 @@
+"""Attention over the whole range of its numbers. Each bound is derived from the
+roundings that the header and the formula's comment state."""
+import math
+
+import pytest
+import torch
+
+import block_ref as R
+from test_gpu_attention import BF16, F16, qkv, run
+
+pytestmark = pytest.mark.gpu
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def sq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_post_quantized_smooth_amd as sq
+    return sq
+
+
+def capped(q, k, v, scale, cap, slopes=None, causal=False):
+    """(out, bound) in fp64 with the cap's error relative to the score.
+
+    A logit's error: D + 4 fp32 roundings of the dot product, 2^-19 of the capped
+    score (tanh, whichever form; caps up to 64 may be off by 8 * 2^-24 of the cap
+    instead), and 4 roundings of the largest logit in base 2. It moves an average
+    of v by twice that times the average of |v|; P and the output are rounded once."""
+    B, Lq, Hq, D = q.shape
+    Lk, Hkv = k.shape[1:3]
+    eps, sub = (2.0 ** -11, 2.0 ** -25) if q.dtype == F16 else (2.0 ** -8, 0.0)
+    q, k, v = (t.cpu().to(F64) for t in (q, k, v))
+    out, bound = (torch.zeros(B, Lq, Hq, D, dtype=F64) for _ in range(2))
+    far = (torch.arange(Lq)[:, None] + Lk - Lq) - torch.arange(Lk)[None]
+    for b in range(B):
+        for h in range(Hq):
+            kk, vv = k[b, :, h // (Hq // Hkv)], v[b, :, h // (Hq // Hkv)]
+            x = (q[b, :, h] @ kk.t().contiguous()) * scale
+            dx = (D + 4) * 2.0 ** -24 * abs(scale) * q[b, :, h].norm(dim=1, keepdim=True) * kk.norm(dim=1).max()
+            x = cap * torch.tanh(x / cap)
+            dx = dx + 2.0 ** -19 * x.abs().amax(1, keepdim=True) + (8 * cap * 2.0 ** -24 if cap <= 64 else 0.0)
+            if slopes is not None:
+                s = float(slopes[h])
+                x = x - s * far.abs()
+                dx = dx + 4 * s * (Lk + Lq) * 2.0 ** -24
+            if causal:
+                x = torch.where(far >= 0, x, -math.inf)
+            dx = dx + 4 * 2.0 ** -24 * (2 + x.amax(1, keepdim=True).abs())
+            p = torch.softmax(x, 1)
+            o, a = p @ vv, p @ vv.abs()
+            out[b, :, h] = o
+            tail = Lk * sub * vv.abs().max() / (p / p.amax(1, keepdim=True)).sum(1, keepdim=True)
+            bound[b, :, h] = eps * (a + o.abs()) + (2 * dx + 2.0 ** -20) * a + tail + sub
+    return out, bound
+
+
+# one row, one row tile of 32 rows and more, and enough sequences for tiles of 128
+SHAPES = [(1, 1, 300, 2, 1, 128), (2, 70, 130, 2, 2, 64), (16, 75, 90, 16, 16, 64)]
+CAPS = [1e-44, 1e-3, 30.0, 64.0, 65.0, 1e3, 1e5, 1e6, 1e7, 1e8, 3e38]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_any_cap(sq, shape, cap, dtype):
+    q, k, v = qkv(*shape, dtype)
+    scale = 2 * shape[5] ** -0.5                         # logits of deviation 2
+    R.assert_within(run(sq, q, k, v, scale=scale, softcap=cap), *capped(q, k, v, scale, cap))
+
+
+@pytest.mark.parametrize("cap", [50.0, 300.0, 1e6])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_a_cap_with_slopes_masks_and_large_scores(sq, shape, cap):
+    q, k, v = qkv(*shape, BF16)
+    sl = torch.logspace(-3, 0, shape[3], device="cuda")
+    R.assert_within(run(sq, q, k, v, scale=-0.1, softcap=cap, slopes=sl, causal=True),
+                    *capped(q, k, v, -0.1, cap, sl, True))
+    # scores from nothing to far beyond the cap in one row
+    ramp = torch.logspace(-4, 3, shape[2], device="cuda")[None, :, None, None]
+    k2 = (k * ramp).to(BF16)
+    R.assert_within(run(sq, q, k2, v, scale=0.1, softcap=cap), *capped(q, k2, v, 0.1, cap))
