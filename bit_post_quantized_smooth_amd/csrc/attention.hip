@@ -149,9 +149,10 @@ struct Attention {
   int hk;
   vec qf[DS];
   v16f o[DB];
-  // the row's reference maximum (base 2) and this half's sum. The reference only
-  // follows the running maximum when that has grown by more than kGrow: until
-  // then exp2(x - m) stays below 2^kGrow and nothing needs rescaling.
+  // the row's reference (base 2) and this half's sum. The reference is the running
+  // maximum rounded up to a whole number, so that rescaling multiplies by a power of
+  // two, which rounds nothing, and only follows it when it has grown by more than
+  // kGrow: until then exp2(x - m) stays below 2^kGrow and nothing needs rescaling.
   float m, l;
   int lo, pos;                                      // the row's first key, its own position
   uint32_t width;                                   // keys it sees, from lo on
@@ -291,7 +292,7 @@ struct Attention {
     return __builtin_amdgcn_ballot_w64(top > m + kGrow) != 0;
   }
   __device__ __forceinline__ float raise(float top) {
-    const float m_new = fmaxf(m, top);
+    const float m_new = fmaxf(m, __builtin_ceilf(top));
     const float alpha = m_new == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
     m = m_new;
     large = __builtin_amdgcn_ballot_w64(m > kLarge || (m < -kLarge && m != kNegInf)) != 0;
@@ -305,10 +306,10 @@ struct Attention {
   // what the exponentials subtract; -inf: a row that has seen no key yet
   __device__ __forceinline__ float base() const { return m == kNegInf ? 0.f : m; }
 
-  // The scale of the exponentials' exp2(scale * x - base) in one rounding. That
-  // leaves a factor of the row, from the rounding of base, which the division by
-  // the sum takes out, unless base is so large that the factor overflows: then
-  // the product is rounded first, as base was.
+  // The scale of the exponentials' exp2(scale * x - base) in one rounding. The
+  // maximum that base comes from was rounded as a product: it can lie below the
+  // product that goes in here, by 2^-4 up to a base of kLarge, but by enough to
+  // overflow beyond. Then the product is rounded first, as the maximum was.
   __device__ __forceinline__ float exp_scale(v16f& x) {
     if constexpr (!RAW) return 1.f;
     if (!large) return g.scale2;
@@ -420,7 +421,7 @@ struct Attention {
     exponentials(x, scale, p);
     __builtin_amdgcn_sched_barrier(0);
     top = half_max(logits<MASK>(y, key0 + 32));
-    if (outgrows(top)) {                 // x's exponentials are not in o yet
+    if (outgrows(top)) {                 // x's exponentials are not in o yet; exact
       const float alpha = raise(top);
 #pragma unroll
       for (int i = 0; i < 16; ++i)

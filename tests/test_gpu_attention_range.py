@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_ref as R
-from test_gpu_attention import BF16, F16, qkv, run
+from test_gpu_attention import BF16, F16, check, qkv, run
 
 pytestmark = pytest.mark.gpu
 F64 = torch.float64
@@ -80,3 +80,17 @@ def test_a_cap_with_slopes_masks_and_large_scores(sq, shape, cap):
     ramp = torch.logspace(-4, 3, shape[2], device="cuda")[None, :, None, None]
     k2 = (k * ramp).to(BF16)
     R.assert_within(run(sq, q, k2, v, scale=0.1, softcap=cap), *capped(q, k2, v, 0.1, cap))
+
+
+def test_weights_are_rounded_once(sq):
+    """32 keys, then 32 that outgrow them while the first block's weights are waiting in
+    16 bits: were those rounded again after their rescaling, the output (all of it
+    theirs) would be off by 2.6 units of its type's precision, where two are allowed."""
+    B, H, L, D = 16, 16, 75, 64
+    q = torch.zeros(B, L, H, D, dtype=F16, device="cuda")
+    k = torch.zeros(B, 64, H, D, dtype=F16, device="cuda")
+    v = torch.zeros_like(k)
+    q[..., 0] = 1.0
+    k[:, 1:32, :, 0], k[:, 32:, :, 0] = -0.58984375, 6.296875
+    v[:, 1:32] = 64.0
+    check(sq, q, k, v, scale=1.0)
