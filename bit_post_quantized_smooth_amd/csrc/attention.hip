@@ -33,8 +33,8 @@
 // along the keys over workgroups, which then write fp32 outputs with their maxima
 // and sums for a second kernel that joins them in order.
 //
-// The maximum that the exponents refer to is raised only when a score exceeds it
-// by 2^8 (kGrow): the outputs are then rescaled, otherwise they stay in place. The
+// The maximum that the exponents refer to is raised only when a score exceeds it by
+// kGrow (4 or 8, base 2): the outputs are then rescaled, otherwise they stay in place. The
 // products of one half of a tile go out beside the exponents of the other. Tiles
 // that no row sees in part run a loop without masks; tiles cut by a mask, and a
 // wave's tiles of which it sees nothing, have loops of their own, since a branch
@@ -66,7 +66,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kWaves = 4;
-constexpr float kGrow = 8.f;         // how far scores may exceed the reference, base 2
 constexpr float kLarge = 1e6f;       // logits (base 2); their rounding is below 2^-4
 
 template <class T>
@@ -77,7 +76,11 @@ struct Half<_Float16> {
   static __device__ __forceinline__ v16f mfma(v8h a, v8h b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
-  static constexpr uint16_t kOne = 0x3C00, kInf = 0x7C00;
+  static constexpr uint16_t kInf = 0x7C00;
+  // What is far below a row's largest weight falls among fp16's subnormal numbers, so
+  // the largest is not 1 but up to 2^11: a weight's step is at most 2^-34 of it, where
+  // it was 2^-24. 2^4 above that the outputs are rescaled, below 65504.
+  static constexpr float kLift = 11.f, kGrow = 4.f;
 };
 template <>
 struct Half<__bf16> {
@@ -85,7 +88,8 @@ struct Half<__bf16> {
   static __device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  static constexpr uint16_t kOne = 0x3F80, kInf = 0x7F80;
+  static constexpr uint16_t kInf = 0x7F80;
+  static constexpr float kLift = 0.f, kGrow = 8.f;
 };
 
 typedef short v4s __attribute__((ext_vector_type(4)));
@@ -151,8 +155,9 @@ struct Attention {
   v16f o[DB];
   // the row's reference (base 2) and this half's sum. The reference is the running
   // maximum rounded up to a whole number, so that rescaling multiplies by a power of
-  // two, which rounds nothing, and only follows it when it has grown by more than
-  // kGrow: until then exp2(x - m) stays below 2^kGrow and nothing needs rescaling.
+  // two, which rounds nothing, less kLift. It only follows the maximum when that has
+  // grown by more than kGrow: until then exp2(x - m) stays below 2^(kLift + kGrow) and
+  // nothing needs rescaling.
   float m, l;
   int lo, pos;                                      // the row's first key, its own position
   uint32_t width;                                   // keys it sees, from lo on
@@ -289,10 +294,10 @@ struct Attention {
   // Whether a block's largest logits (the row's, of both halves) outgrow the
   // reference in any row; the new reference if so.
   __device__ __forceinline__ bool outgrows(float top) const {
-    return __builtin_amdgcn_ballot_w64(top > m + kGrow) != 0;
+    return __builtin_amdgcn_ballot_w64(top > m + (Half<T>::kLift + Half<T>::kGrow)) != 0;
   }
   __device__ __forceinline__ float raise(float top) {
-    const float m_new = fmaxf(m, __builtin_ceilf(top));
+    const float m_new = fmaxf(m, __builtin_ceilf(top) - Half<T>::kLift);
     const float alpha = m_new == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
     m = m_new;
     large = __builtin_amdgcn_ballot_w64(m > kLarge || (m < -kLarge && m != kNegInf)) != 0;

@@ -737,6 +737,8 @@ size_t svdq_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t
  *   (prefix: NULL or one int32 per batch entry; only with causal).
  * A row that sees no key is 0; a key that a row does not see does not reach its
  * output even where its K or V hold infinities or NaN.
+ * Scores, maxima, sums and outputs are fp32; a softmax weight is rounded once to the
+ * type of V, in f16 to a multiple of at most 2^-34 of the row's largest weight.
  * dtype (f16, bf16) is that of Q, K, V and Out. Query head h reads key head
  * h / (Hq / Hkv). `strides`: 12 element strides, (batch, token, head) of Q, K, V
  * and Out in that order; channels are contiguous. Each is a multiple of 8 and

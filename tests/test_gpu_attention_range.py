@@ -82,6 +82,32 @@ def test_a_cap_with_slopes_masks_and_large_scores(sq, shape, cap):
     R.assert_within(run(sq, q, k2, v, scale=0.1, softcap=cap), *capped(q, k2, v, 0.1, cap))
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 4096, 1, 1, 64), (1, 40, 4096, 2, 2, 64), (16, 75, 1024, 16, 16, 64)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("nats", [8.0, 14.0, 17.0, 17.5, 20.0])
+@pytest.mark.parametrize("at", [0, -1], ids=["first", "last"])
+def test_many_small_weights_beside_one_large(sq, shape, nats, at):
+    """A key far above all others whose V is 0, as models learn them: the output is what
+    the others bring, whose weights are down to e^-21 of the row's largest. fp16 weights
+    are multiples of 2^-34 of the largest at the coarsest: half of that step for every
+    key, besides one rounding each of the weight and the output, and the error of a
+    logit (D + 4 roundings of the product, 4 in base 2)."""
+    B, Lq, Lk, Hq, Hkv, D = shape
+    q, k, v = qkv(*shape, F16)
+    q[..., 0], q[..., 1:] = 1.0, 0.0
+    k[..., 0], k[..., 1:] = -torch.rand(k.shape[:3], generator=torch.Generator().manual_seed(1)).cuda(), 0.0
+    k[:, at, :, 0] = nats
+    v = (64.0 + 8 * v).clamp(0, 128).to(F16)
+    v[:, at] = 0
+    got = run(sq, q, k, v, scale=1.0).cpu().to(F64)
+    w = torch.exp(k[..., :1].cpu().to(F64) - nats)
+    total = w.sum(1, keepdim=True)
+    o = ((w * v.cpu().to(F64)).sum(1, keepdim=True) / total).expand(B, Lq, Hq, D)
+    dx = (D + 4) * 2.0 ** -24 * nats + 4 * 2.0 ** -24 * (2 + nats)
+    bound = 2.0 ** -11 * 2 * o + 2 * dx * o + (Lk - 1) * 2.0 ** -35 * 128 / total + 2.0 ** -25
+    R.assert_within(got, o, bound)
+
+
 def test_weights_are_rounded_once(sq):
     """32 keys, then 32 that outgrow them while the first block's weights are waiting in
     16 bits: were those rounded again after their rescaling, the output (all of it
