@@ -81,6 +81,7 @@ struct Half<_Float16> {
   // the largest is not 1 but up to 2^11: a weight's step is at most 2^-34 of it, where
   // it was 2^-24. 2^4 above that the outputs are rescaled, below 65504.
   static constexpr float kLift = 11.f, kGrow = 4.f;
+  static constexpr float kCarefulLift = kLift;      // no sum of fp16 values is that large
 };
 template <>
 struct Half<__bf16> {
@@ -90,6 +91,9 @@ struct Half<__bf16> {
   }
   static constexpr uint16_t kInf = 0x7F80;
   static constexpr float kLift = 0.f, kGrow = 8.f;
+  // In the careful pass: sums of values near the type's (and fp32's) largest stay finite
+  // where each weight is at most 2^-24, for up to 2^24 keys.
+  static constexpr float kCarefulLift = -32.f;
 };
 
 typedef short v4s __attribute__((ext_vector_type(4)));
@@ -293,11 +297,17 @@ struct Attention {
 
   // Whether a block's largest logits (the row's, of both halves) outgrow the
   // reference in any row; the new reference if so.
-  __device__ __forceinline__ bool outgrows(float top) const {
-    return __builtin_amdgcn_ballot_w64(top > m + (Half<T>::kLift + Half<T>::kGrow)) != 0;
+  template <bool CAREFUL>
+  static constexpr float lift() {
+    return CAREFUL ? Half<T>::kCarefulLift : Half<T>::kLift;
   }
+  template <bool CAREFUL>
+  __device__ __forceinline__ bool outgrows(float top) const {
+    return __builtin_amdgcn_ballot_w64(top > m + (lift<CAREFUL>() + Half<T>::kGrow)) != 0;
+  }
+  template <bool CAREFUL>
   __device__ __forceinline__ float raise(float top) {
-    const float m_new = fmaxf(m, __builtin_ceilf(top) - Half<T>::kLift);
+    const float m_new = fmaxf(m, __builtin_ceilf(top) - lift<CAREFUL>());
     const float alpha = m_new == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
     m = m_new;
     large = __builtin_amdgcn_ballot_w64(m > kLarge || (m < -kLarge && m != kNegInf)) != 0;
@@ -403,7 +413,7 @@ struct Attention {
   __device__ __forceinline__ void block(int s, int row0, int key0) {
     v16f x = products(k_at(s), row0);
     const float top = half_max(logits<true>(x, key0));
-    if (outgrows(top)) raise(top);
+    if (outgrows<CAREFUL>(top)) raise<CAREFUL>(top);
     vec p[2];
     const float scale = exp_scale(x);
     exponentials(x, scale, p);
@@ -420,14 +430,14 @@ struct Attention {
     v16f x = products(ka, row0);
     vec p[2], r[2];
     float top = half_max(logits<MASK>(x, key0));
-    if (outgrows(top)) raise(top);
+    if (outgrows<false>(top)) raise<false>(top);
     float scale = exp_scale(x);
     v16f y = products(ka, row0 + 32);
     exponentials(x, scale, p);
     __builtin_amdgcn_sched_barrier(0);
     top = half_max(logits<MASK>(y, key0 + 32));
-    if (outgrows(top)) {                 // x's exponentials are not in o yet; exact
-      const float alpha = raise(top);
+    if (outgrows<false>(top)) {          // x's exponentials are not in o yet; exact
+      const float alpha = raise<false>(top);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         p[i >> 3][i & 7] = static_cast<T>(static_cast<float>(p[i >> 3][i & 7]) * alpha);
@@ -609,8 +619,9 @@ struct Attention {
       qf[s] = __builtin_bit_cast(vec, z);
     }
     // A hidden key has P = 0, but 0 times an infinity or a NaN in V would reach the
-    // rows that do not see it. That leaves a NaN, so the first pass does not look
-    // at V; only where an output is not finite a second one does.
+    // rows that do not see it, and a sum of bf16 values can overflow where their average
+    // does not. Both leave an output that is not finite, so the first pass does not look
+    // at V; only then a second one does, with lower weights.
     pass<false>(first, last, t0, t1);
     bool odd = false;
 #pragma unroll
@@ -653,7 +664,8 @@ struct Attention {
     float top = kNegInf;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml[(w * 32 + rl) * 2]);
-    const float base = top == kNegInf ? 0.f : top;
+    // two above the largest: the sum of four finite partial outputs is finite
+    const float base = top == kNegInf ? 0.f : top + 2.f;
     float f[kWaves];
     l = 0.f;
 #pragma unroll
@@ -661,7 +673,7 @@ struct Attention {
       f[w] = __builtin_amdgcn_exp2f(ml[(w * 32 + rl) * 2] - base);
       l = __builtin_fmaf(ml[(w * 32 + rl) * 2 + 1], f[w], l);
     }
-    m = top;
+    m = top == kNegInf ? top : base;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -744,7 +756,8 @@ __global__ __launch_bounds__(32 * kJoin) void attention_join(const AttnArgs g) {
   float top = m;
 #pragma unroll
   for (int d = 32; d >= 1; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
-  const float f = l == 0.f ? 0.f : __builtin_amdgcn_exp2f(m - (top == kNegInf ? 0.f : top));
+  // 2^6 splits at most: the sum of their finite partial outputs is finite
+  const float f = l == 0.f ? 0.f : __builtin_amdgcn_exp2f(m - (top == kNegInf ? 0.f : top + 6.f));
   v4f o = v4f{0.f, 0.f, 0.f, 0.f};
   float n = 0.f;
 #pragma unroll

@@ -120,3 +120,23 @@ def test_weights_are_rounded_once(sq):
     k[:, 1:32, :, 0], k[:, 32:, :, 0] = -0.58984375, 6.296875
     v[:, 1:32] = 64.0
     check(sq, q, k, v, scale=1.0)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 300, 2, 1, 64), (1, 3, 5000, 2, 2, 128), (2, 70, 130, 2, 2, 64),
+                                   (16, 75, 200, 16, 16, 64)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("most", [3e38, 1e36])
+def test_values_near_the_end_of_bf16(sq, shape, most):
+    """Averages of values that are finite, but whose sums are not."""
+    q, k, v = qkv(*shape, BF16)
+    v = (v.sign() * most).to(BF16)
+    for ws in (True, False):
+        check(sq, q, k, v, ws=ws)
+        check(sq, q, k, v.abs(), ws=ws, causal=True)
+
+
+def test_the_largest_fp16_values(sq):
+    """An average of 65504 is 65504 in every row."""
+    q, k, v = qkv(2, 70, 300, 2, 2, 64, F16)
+    v.fill_(65504.0)
+    out = run(sq, q, k, v)
+    assert bool((out >= 65472).all()) and bool(torch.isfinite(out).all())
