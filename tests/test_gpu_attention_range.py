@@ -140,3 +140,20 @@ def test_the_largest_fp16_values(sq):
     v.fill_(65504.0)
     out = run(sq, q, k, v)
     assert bool((out >= 65472).all()) and bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("shape", [(2, 1, 40, 4, 2, 128), (1, 70, 70, 2, 2, 64), (16, 75, 90, 16, 16, 64)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_a_row_that_sees_one_key_is_its_value(sq, shape, dtype):
+    """And a row of equal values is that value, up to the last ones that fp16 has: the
+    weights add up to 1 after their rounding."""
+    B, Lq, Lk, Hq, Hkv, D = shape
+    q, k, v = qkv(*shape, dtype)
+    r = torch.zeros(1, Lq, 2, dtype=torch.int32)
+    r[0, :, 0] = torch.arange(Lq) % Lk
+    r[0, :, 1] = r[0, :, 0] + 1
+    out = run(sq, q, k, v, key_ranges=r.cuda())
+    assert torch.equal(out, v[:, r[0, :, 0].long().cuda()].repeat_interleave(Hq // Hkv, 2))
+    v = torch.where(v > 0, 65504.0, -65504.0)[:, :1].expand_as(v).to(dtype).contiguous()
+    assert torch.equal(run(sq, q, k, v), v[:, :1].repeat_interleave(Hq // Hkv, 2).expand_as(q))
