@@ -32,8 +32,18 @@ class KeyValueCache:
         self.length = 0
 
     def append(self, k, v):
-        """Take in k and v (batch x tokens x kv_heads x head_dim); the views of all
-        tokens held."""
+        """Take in k and v (batch x tokens x kv_heads x head_dim, the cache's type); the
+        views of all tokens held. What does not fit is refused before anything changes."""
+        torch = api._torch()
+        for name, t in (("k", k), ("v", v)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+            want = (self.k.shape[0], k.shape[1] if k.dim() == 4 else None, *self.k.shape[2:])
+            if tuple(t.shape) != want:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, the cache takes {want}")
+            if t.dtype != self.k.dtype or t.device != self.k.device:
+                raise ValueError(f"{name}: {t.dtype} on {t.device}, the cache holds {self.k.dtype} "
+                                 f"on {self.k.device}")
         end = self.length + k.shape[1]
         if end > self.k.shape[1]:
             raise ValueError(f"cache of {self.k.shape[1]} tokens: {end} needed")
@@ -51,7 +61,7 @@ class AttentionBlock:
     ``block(X, residual)`` takes batch x tokens x K and returns (Y, h): the
     block's output and X + residual, which are the next block's X and residual.
     With a KeyValueCache the tokens are appended to it and attend to all that it
-    holds. Buffers are kept between calls and grown when more tokens arrive, so
+    holds; a call that raises leaves the cache's length as it was. Buffers are kept between calls and grown when more tokens arrive, so
     one block serves one stream at a time, and Y and h are new tensors."""
 
     def __init__(self, gain, qkv, out, heads: int, kv_heads: int, head_dim: int,
@@ -110,6 +120,16 @@ class AttentionBlock:
             raise ValueError(f"X: shape {tuple(X.shape)}, expected (batch, tokens, {self.K})")
         if residual is not None and residual.shape != X.shape:
             raise ValueError(f"residual: shape {tuple(residual.shape)}, X has {tuple(X.shape)}")
+        held = None if cache is None else cache.length
+        try:
+            return self._run(X, residual, cache, causal, prefix, key_ranges)
+        except BaseException:
+            if cache is not None:
+                cache.length = held      # tokens behind it are not seen and written again
+            raise
+
+    def _run(self, X, residual, cache, causal, prefix, key_ranges):
+        torch = api._torch()
         B, L, K = X.shape
         M, D, Hq, Hkv = B * L, self.head_dim, self.heads, self.kv_heads
         h = torch.empty_like(X, memory_format=torch.contiguous_format)

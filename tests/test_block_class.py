@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import bit_post_quantized_smooth_amd as sq
+from bit_post_quantized_smooth_amd import block as block_module
 
 
 def weights(K=256, Hq=4, Hkv=2, D=32):
@@ -50,3 +51,34 @@ def test_cache():
     with pytest.raises(ValueError, match="cache of 10"):
         c.append(a, a)
     assert c.length == 8
+
+
+def test_cache_refuses_what_does_not_fit():
+    """A batch of one is not spread over the sequences, another type is not converted:
+    what is held stays as it was."""
+    c = sq.KeyValueCache(2, 10, 3, 8, torch.float16, device="cpu")
+    a = torch.ones(2, 4, 3, 8, dtype=torch.float16)
+    c.append(a, a)
+    held = c.k.clone(), c.v.clone()
+    for k, v in ((a[:1], a[:1]), (a, a[:, :1]), (a[:, :, :1], a), (a, a[..., :1]), (a[0], a[0]),
+                 (a.float(), a.float()), (a, a.bfloat16()), (a.to("meta"), a)):
+        with pytest.raises(ValueError, match="k: |v: "):
+            c.append(k, v)
+    with pytest.raises(TypeError):
+        c.append(a.numpy(), a)
+    assert c.length == 4 and torch.equal(c.k[:, :4], held[0][:, :4]) and torch.equal(c.v[:, :4], held[1][:, :4])
+
+
+def test_a_refused_call_leaves_the_cache_as_it_was(monkeypatch):
+    """Attention's refusals come behind the append: the length goes back."""
+    block = sq.AttentionBlock(np.ones(256, np.float32), *weights(), 4, 2, 32, device="cpu")
+    for f in ("rmsnorm_quantize_fp8", "gemm_fp8", "quantize_act_fp8"):
+        monkeypatch.setattr(block_module.api, f, lambda *a, **k: None)
+    X = torch.zeros(2, 3, 256, dtype=torch.float16)
+    cache = sq.KeyValueCache(2, 10, 2, 32, torch.float16, device="cpu")
+    for kw, match in ((dict(causal=False, prefix=torch.zeros(2, dtype=torch.int32)), "prefix"),
+                      (dict(key_ranges=torch.zeros(3, 3, 2, dtype=torch.int32)), "key_ranges"),
+                      (dict(), "on a GPU")):
+        with pytest.raises(ValueError, match=match):
+            block(X, cache=cache, **kw)
+        assert cache.length == 0
