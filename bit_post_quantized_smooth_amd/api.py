@@ -1185,6 +1185,9 @@ class Linear:
     def __init__(self, prep: Prepared, bias: Optional[np.ndarray] = None, device="cuda",
                  out_dtype=None, activation=None, tiled: bool = False):
         torch = _torch()
+        if prep.fmt == "fp8" and prep.rank:
+            raise ValueError(f"an 8-bit layer has no low-rank branch: this prep's, of rank "
+                             f"{prep.rank}, would not be applied")
         self.K, self.N, self.R = prep.K, prep.N, prep.rank
         dev = torch.device(device)
         self.inv_smooth = torch.from_numpy(prep.inv_smooth).to(dev)

@@ -71,6 +71,9 @@ class AttentionBlock:
         self.K = qkv.K
         if qkv.fmt != "fp8" or out.fmt != "fp8":
             raise ValueError("qkv and out must come from prepare_weights_fp8")
+        if qkv.rank or out.rank:
+            raise ValueError("8-bit layers have no low-rank branch: qkv's or out's would not be "
+                             "applied")
         if qkv.N != (heads + 2 * kv_heads) * head_dim or out.K != heads * head_dim or out.N != qkv.K:
             raise ValueError(f"qkv is {qkv.K} x {qkv.N} and out {out.K} x {out.N}: they do not fit "
                              f"{heads} + 2 x {kv_heads} heads of {head_dim}")

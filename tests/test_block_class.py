@@ -1,4 +1,6 @@
 """The attention block's refusals, and its cache, without a GPU."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -82,3 +84,18 @@ def test_a_refused_call_leaves_the_cache_as_it_was(monkeypatch):
         with pytest.raises(ValueError, match=match):
             block(X, cache=cache, **kw)
         assert cache.length == 0
+
+
+def test_a_low_rank_branch_is_not_dropped():
+    """concat_lora on an 8-bit prep gives a branch that no 8-bit layer applies."""
+    qkv, out = weights()
+    rng = np.random.default_rng(1)
+    A, B = rng.standard_normal((256, 16)), rng.standard_normal((16, 256))
+    lora = sq.concat_lora(sq.prepare_weights_fp8(np.ones((256, 256), np.float32)), np.ones(256), A, B)
+    assert lora.rank == 16
+    with pytest.raises(ValueError, match="low-rank"):
+        sq.Linear(lora, device="cpu")
+    both = dict(rank=16, L1t=np.zeros((16, 256), np.uint16), L2t=np.zeros((256, 16), np.uint16))
+    for a, b in ((dataclasses.replace(qkv, **both), out), (qkv, dataclasses.replace(out, **both))):
+        with pytest.raises(ValueError, match="low-rank"):
+            sq.AttentionBlock(np.ones(256, np.float32), a, b, 4, 2, 32, device="cpu")
