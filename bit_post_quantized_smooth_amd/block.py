@@ -77,6 +77,14 @@ class AttentionBlock:
         if qkv.N != (heads + 2 * kv_heads) * head_dim or out.K != heads * head_dim or out.N != qkv.K:
             raise ValueError(f"qkv is {qkv.K} x {qkv.N} and out {out.K} x {out.N}: they do not fit "
                              f"{heads} + 2 x {kv_heads} heads of {head_dim}")
+        if (min(heads, kv_heads, head_dim) < 1 or heads % kv_heads or head_dim % 8
+                or head_dim > 128):
+            raise ValueError(f"{heads} heads over {kv_heads} of {head_dim}: attention takes whole "
+                             "groups of heads, each a multiple of 8 up to 128")
+        for name, x, n in (("gain", gain, qkv.K), ("qkv_bias", qkv_bias, qkv.N),
+                           ("out_bias", out_bias, out.N), ("slopes", slopes, heads)):
+            if x is not None and math.prod(np.shape(x)) != n:
+                raise ValueError(f"{name}: shape {tuple(np.shape(x))}, expected {n} values")
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.eps, self.softcap = float(eps), float(softcap)
         dev = self.device = torch.device(device)

@@ -99,3 +99,22 @@ def test_a_low_rank_branch_is_not_dropped():
     for a, b in ((dataclasses.replace(qkv, **both), out), (qkv, dataclasses.replace(out, **both))):
         with pytest.raises(ValueError, match="low-rank"):
             sq.AttentionBlock(np.ones(256, np.float32), a, b, 4, 2, 32, device="cpu")
+
+
+@pytest.mark.parametrize("heads,kv_heads,D", [(3, 2, 32), (4, 2, 20), (4, 2, 136), (0, 2, 32), (4, 0, 32), (4, -2, 32)])
+def test_heads_that_attention_does_not_take(heads, kv_heads, D):
+    """Refused when the block is made, not when its first call has done half its work."""
+    n = max(heads + 2 * kv_heads, 1) * D
+    f = lambda *s: np.ones(s, np.float32)  # noqa: E731
+    with pytest.raises(ValueError):
+        sq.AttentionBlock(f(256), sq.prepare_weights_fp8(f(256, n)), sq.prepare_weights_fp8(f(max(heads, 1) * D, 256)),
+                          heads, kv_heads, D, device="cpu")
+
+
+@pytest.mark.parametrize("over", [dict(gain=255), dict(qkv_bias=255), dict(out_bias=1), dict(slopes=2)])
+def test_vectors_of_another_length(over):
+    a = dict(gain=np.ones(256, np.float32))
+    a.update({k: np.ones(n, np.float32) for k, n in over.items()})
+    qkv, out = weights()
+    with pytest.raises(ValueError, match=next(iter(over))):
+        sq.AttentionBlock(qkv=qkv, out=out, heads=4, kv_heads=2, head_dim=32, device="cpu", **a)
