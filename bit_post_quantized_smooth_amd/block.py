@@ -62,7 +62,8 @@ class AttentionBlock:
     block's output and X + residual, which are the next block's X and residual.
     With a KeyValueCache the tokens are appended to it and attend to all that it
     holds; a call that raises leaves the cache's length as it was. Buffers are kept between calls and grown when more tokens arrive, so
-    one block serves one stream at a time, and Y and h are new tensors."""
+    one block serves one stream at a time (those that a graph capture has used stay
+    for its replays), and Y and h are new tensors."""
 
     def __init__(self, gain, qkv, out, heads: int, kv_heads: int, head_dim: int,
                  qkv_bias=None, out_bias=None, eps: float = 1e-6, softcap: float = 0.0,
@@ -95,15 +96,13 @@ class AttentionBlock:
         self.gain, self.slopes = put(gain), put(slopes)
         self.qkv = (torch.from_numpy(qkv.w_codes).to(dev), put(qkv.w_scales), put(qkv_bias))
         self.out = (torch.from_numpy(out.w_codes).to(dev), put(out.w_scales), put(out_bias))
-        self._kept = {}
+        self._buffers = api._Buffers(dev)
+        self._kept = self._buffers.kept
 
     def _buffer(self, name, shape, dtype):
         """The buffer kept under `name`, as a tensor of this shape."""
         count = math.prod(shape)
-        t = self._kept.get((name, dtype))
-        if t is None or t.numel() < count:
-            t = self._kept[name, dtype] = api._torch().empty(count, dtype=dtype, device=self.device)
-        return t[:count].view(shape)
+        return self._buffers.get(name, count, dtype)[:count].view(shape)
 
     def _codes(self, name, M, K):
         torch = api._torch()
