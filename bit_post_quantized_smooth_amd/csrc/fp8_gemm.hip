@@ -551,56 +551,42 @@ constexpr int kRowWaves = 8;
 template <int YT, bool GELU>
 __global__ __launch_bounds__(64 * kRowWaves) void gemm_fp8_rows(const GemmArgs g) {
   constexpr bool EXACT = YT == SVDQ_F32;
-  constexpr int NBM = 1;
-  __shared__ v4f sums[kRowWaves][NBM][64];
+  __shared__ v4f sums[kRowWaves][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int rl = lane & 15, q = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
   const int C = static_cast<int>(g.Kp / kChunk);
   const int64_t n = n0 + rl < g.N ? n0 + rl : g.N - 1;
+  const int64_t m = rl < g.M ? rl : g.M - 1;
   const uint8_t* w = g.w + n * g.Kp + 32 * q;
-  const uint8_t* a[NBM];
-  const float* sa[NBM];
-#pragma unroll
-  for (int i = 0; i < NBM; ++i) {
-    const int64_t m = 16 * i + rl < g.M ? 16 * i + rl : g.M - 1;
-    a[i] = g.a + m * g.Kp + 32 * q;
-    sa[i] = g.sa + m * C;
-  }
+  const uint8_t* a = g.a + m * g.Kp + 32 * q;
+  const float* sa = g.sa + m * C;
   const float* sw = g.sw + (n0 / kFp8Block) * C;
-  v4f acc[NBM];
-#pragma unroll
-  for (int i = 0; i < NBM; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
   for (int c = wave; c < C; c += kRowWaves) {
     const int64_t at = static_cast<int64_t>(c) * kChunk;
     const v4i* wp = reinterpret_cast<const v4i*>(w + at);
-    Frag<EXACT> fw;
+    const v4i* ap = reinterpret_cast<const v4i*>(a + at);
+    Frag<EXACT> fw, fa;
     fw.set(wp[0], wp[1]);
+    fa.set(ap[0], ap[1]);
+    const float scale = sa[c] * sw[c];
+    const v4f p = mfma_group(fw, fa);
 #pragma unroll
-    for (int i = 0; i < NBM; ++i) {
-      const v4i* ap = reinterpret_cast<const v4i*>(a[i] + at);
-      Frag<EXACT> fa;
-      fa.set(ap[0], ap[1]);
-      const float scale = sa[i][c] * sw[c];
-      const v4f p = mfma_group(fw, fa);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(p[e], scale, acc[i][e]);
-    }
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(p[e], scale, acc[e]);
   }
-#pragma unroll
-  for (int i = 0; i < NBM; ++i) sums[wave][i][lane] = acc[i];
+  sums[wave][lane] = acc;
   __syncthreads();
-  for (int i = wave; i < NBM; i += kRowWaves) {
-    v4f v = sums[0][i][lane];
+  if (wave != 0) return;
+  v4f v = sums[0][lane];
 #pragma unroll
-    for (int s = 1; s < kRowWaves; ++s) {
-      const v4f o = sums[s][i][lane];
+  for (int s = 1; s < kRowWaves; ++s) {
+    const v4f o = sums[s][lane];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = v[e] + o[e];
-    }
-    finish4<YT, GELU>(g, v, bias4(g, n0 + 4 * q), 16 * i + rl, n0 + 4 * q);
+    for (int e = 0; e < 4; ++e) v[e] = v[e] + o[e];
   }
+  finish4<YT, GELU>(g, v, bias4(g, n0 + 4 * q), rl, n0 + 4 * q);
 }
 
 constexpr int kFewRows = 16;
