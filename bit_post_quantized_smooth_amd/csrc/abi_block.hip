@@ -3,9 +3,11 @@
 // on an error nothing is launched or written.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <limits>
+#include <utility>
 
 #include "../../include/svdq.h"
 #include "attention.hpp"
@@ -234,6 +236,20 @@ int check_attention_sizes(const char* fn, int64_t B, int64_t Lq, int64_t Lk, int
   return SVDQ_OK;
 }
 
+// Whether tokens of B x L x H heads of D channels at these strides may share elements:
+// dimensions by growing stride, each has to step over all that the smaller ones span.
+bool overlaps(const int64_t* strides, int64_t B, int64_t L, int64_t H, int64_t D) {
+  std::pair<int64_t, int64_t> dims[3] = {{strides[0], B}, {strides[1], L}, {strides[2], H}};
+  std::sort(dims, dims + 3);
+  __int128 span = D;                   // 2^30 of 2^40 would not fit 64 bits
+  for (const auto& [stride, count] : dims) {
+    if (count < 2) continue;
+    if (stride < span) return true;
+    span += static_cast<__int128>(count - 1) * stride;
+  }
+  return false;
+}
+
 // Per split and row: the maximum and sum, then D outputs.
 size_t attention_ml_bytes(int64_t B, int64_t Lq, int64_t Hq, int splits) {
   return round_up(static_cast<size_t>(splits) * B * Lq * Hq * 8, 256);
@@ -276,6 +292,8 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
   if (sk[1] > kMaxK || sv[1] > kMaxK || (Lk > 1 && (sk[1] < D || sv[1] < D)))
     return fail(SVDQ_ERR_SHAPE, fn, "token strides of K and V must lie in D .. 2^22");
   if (B == 0 || Lq == 0) return SVDQ_OK;
+  if (overlaps(strides + 9, B, Lq, Hq, D))
+    return fail(SVDQ_ERR_SHAPE, fn, "the strides of Out make it overlap itself");
   AttnPlan p = attention_plan(B, Lq, Lk, Hq, Hkv, D, true);
   if (p.grid == 0) return fail(SVDQ_ERR_SHAPE, fn, "more rows than one launch can cover");
   if (!Q || !Out || (Lk > 0 && (!K || !V))) return fail(SVDQ_ERR_NULL, fn, "null pointer");

@@ -745,7 +745,7 @@ size_t svdq_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t
  * each pointer 16-byte aligned; token strides of K and V are at most 2^22, and
  * at least D where Lk > 1. D: a multiple of 8 up to 128. key_ranges_batch:
  * elements between the ranges of two batch entries (0: shared). Out may not
- * overlap the inputs. ws: NULL or a 16-byte aligned workspace; with at least
+ * overlap the inputs, nor itself (SVDQ_ERR_SHAPE). ws: NULL or a 16-byte aligned workspace; with at least
  * svdq_attention_workspace_bytes bytes few rows over many keys are split along
  * the keys. */
 int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int dtype, int64_t B,

@@ -1,5 +1,6 @@
 """Products and attentions of more rows than a launch's 2^32 threads cover are refused
-on the host: a launch of more would run a part of them and report nothing."""
+on the host, where a launch of more would run a part of them and report nothing, and
+so are outputs that overlap themselves."""
 import ctypes as C
 
 import pytest
@@ -39,3 +40,17 @@ def test_attention():
 
 def test_workspace_of_what_is_refused():
     assert sq.attention_workspace_bytes(1 << 20, 1, 1, 16, 16, 8) == 0
+
+
+def test_attention_output_over_itself():
+    """Rows written to one place by several workgroups would hold any one of them."""
+    def out(B, L, H, D, *strides):
+        s = [H * L * D, H * D, D] * 3 + list(strides)
+        return _lib.lib.svdq_attention(None, P, P, P, 1, B, L, L, H, H, D, (C.c_int64 * 12)(*s), 1.0, 0.0, None, 0, None,
+                                       None, 0, None, 0, None)
+    good = [(2, 5, 3, 16, 240, 48, 16), (2, 5, 3, 16, 240, 16, 80), (2, 5, 3, 16, 48, 96, 16), (1, 5, 3, 16, 0, 48, 16),
+            (2, 1, 3, 16, 48, 0, 16), (2, 5, 1, 16, 80, 16, 0), (3, 5, 2, 8, 1000, 64, 24)]
+    bad = [(2, 5, 3, 16, 0, 48, 16), (2, 5, 3, 16, 240, 0, 16), (2, 5, 3, 16, 240, 48, 0), (2, 5, 3, 16, 240, 48, 8),
+           (2, 5, 3, 16, 232, 48, 16), (2, 5, 3, 16, 240, 40, 16)]
+    assert [out(*g) for g in good] == [_lib.ERR_NULL] * len(good)
+    assert [out(*b) for b in bad] == [_lib.ERR_SHAPE] * len(bad)
