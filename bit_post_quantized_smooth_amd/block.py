@@ -7,9 +7,11 @@ transformer runs them.
     o = attention(q, keys, values)               attention
     Y = quantize(o) Wout^T + b                   quantize_act_fp8, gemm_fp8
 
-Five launches (more where a product or the attention is split). The normalized
-activation exists only as codes and scales, the residual addition costs no pass
-of its own, and q, k and v are read in place as strided views of one product.
+Five launches (more where a product or the attention is split, and two copies where
+there is a cache). The normalized activation exists only as codes and scales, the
+residual addition costs no pass of its own, and q, k and v are read in place as strided
+views of one product. What a model does to q and k in between (rotary embedding, norms)
+has no place here: such a model calls the operators one by one.
 """
 from __future__ import annotations
 
@@ -22,7 +24,10 @@ from . import api
 
 class KeyValueCache:
     """Keys and values of up to ``capacity`` tokens for each of ``batch``
-    sequences; ``length`` tokens are held."""
+    sequences; ``length`` tokens are held. The length is a number of the host's: a graph
+    captured from a call with the cache writes, in every replay, to the slots of its
+    capture and sees as many keys as it did then. A graph for each length, or eager
+    calls, generate token after token."""
 
     def __init__(self, batch: int, capacity: int, kv_heads: int, head_dim: int, dtype, device="cuda"):
         torch = api._torch()

@@ -43,13 +43,13 @@
 // weight of 0 is NaN where V is not finite: only if an output comes out so is the
 // pass repeated with hidden keys' V taken out.
 //
-// Measured (D = 128). 24 heads of 4608 x 4608, fp16: 288 to 312 us by card, 840 to
-// 900 TFLOP/s; the matrix core is busy 42% of the time, beside 6.5 vector
+// Measured (D = 128). 24 heads of 4608 x 4608, fp16: 286 to 313 us by card, 830 to
+// 910 TFLOP/s; the matrix core is busy 41% of the time, beside 6.5 vector
 // instructions per matrix instruction, and 864 workgroups are 1.69 rounds of the
-// 512 that fit. Packed documents of the same length: 135 us. 16 heads over 4, 8191
-// causal rows with a prefix and capped scores, bf16: 360 to 415 us, the cap's
-// exponential and reciprocal doubling the vector work per score. One token, 32
-// heads over 8, 8 caches of 8191: 42 us plus 5 us to join, 210 MB at 5.0 TB/s.
+// 512 that fit. Packed documents of the same length: 130 to 140 us. 16 heads over 4,
+// 8191 causal rows with a prefix, bf16: 298 us, with scores capped at 30 338 to 383 us
+// by card (350 beside the 298), 11 vector instructions per matrix instruction. One
+// token, 32 heads over 8, 8 caches of 8191: 42 us plus 5 us to join, 210 MB at 5.0 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -272,7 +272,7 @@ struct Attention {
   // but 0.1 at 1e6), so below |y| = 1/4 it is y (1 + u (c1 + c2 u)), u = y^2, with the
   // coefficients of least largest error over that range (5e-7). c1 and c2 are those for
   // t = (2 log2(e) y)^2. Both forms for every score cost more vector work (16 heads over
-  // 4, 8191 causal rows with a prefix, bf16: 441 us against 361), so caps up to kNearest
+  // 4, 8191 causal rows with a prefix, bf16: 435 us against 350), so caps up to kNearest
   // keep the one.
   __device__ __forceinline__ float any_cap(float v) const {
     constexpr float kSmall = 0.25f * 2.0f * kLog2e, c1 = -0.04002727f, c2 = 0.001857806f;
@@ -534,11 +534,14 @@ struct Attention {
     const int rw = wave / KW;
     int t, rt;
     if (RW > 1 && (g.causal || g.ranges != nullptr)) {
-      // Row tiles of unequal work: the last rows first, which see the most keys
-      // where masks follow the order of the tokens, so that what is left at the end
-      // is short; heads next to each other, so that each of the 8 XCDs (to which
-      // workgroups are dealt in turn) gets long and short rows alike. Prefix mask,
-      // 8191 tokens: 555 -> 415 us; causal, 8192: 350 -> 288 us.
+      // Row tiles of unequal work: heads next to each other, so that each of the 8
+      // XCDs (to which workgroups are dealt in turn) gets long and short rows alike,
+      // and the last rows first. Under the causal rule those see the most keys, so
+      // that what is left at the end is short: prefix mask, 8191 tokens: 555 -> 415
+      // us; causal, 8192: 350 -> 288 us. Ranges alone follow no order: heads side by
+      // side take 4608 tokens in documents of 744, 1488 and 2232 from 154 to 135 us,
+      // of falling length from 157 to 125, and 12 of growing or falling length from
+      // 74 and 67 to 57 and 63; the first rows first would give 127, 132, 65 and 57.
       const int heads = g.B * g.Hkv * g.splits;
       t = static_cast<int>(blockIdx.x) % heads;
       rt = g.row_tiles - 1 - static_cast<int>(blockIdx.x) / heads;

@@ -11,10 +11,11 @@
 // for the whole wave.
 //
 // Precision. The 8-bit matrix instructions align the products of one
-// instruction to the largest before they add them: 1e-5 to 5e-5 of |P_g| is
-// lost (measured against fp64 on Gaussian and heavy-tailed groups; the
-// accumulators across groups are fp32). That lies under an fp16 or bf16
-// output's own rounding. An fp32 output takes the variant that widens the
+// instruction to the largest before they add them. What is lost goes by the
+// group's largest |a w|, not by its sum: at most 2^-13 of it in 60000 sums against
+// fp64, which was 1e-5 to 5e-5 of |P_g| on Gaussian and heavy-tailed groups and is
+// more where a group's products cancel (the accumulators across groups are fp32).
+// 16-bit outputs accept that; an fp32 output takes the variant that widens the
 // codes to fp16 (exact) and multiplies with v_mfma_f32_16x16x32_f16, whose
 // sums are good to 1e-7, at half the matrix rate (EXACT below).
 //
@@ -35,8 +36,8 @@
 // 648 tiles are 2.53 rounds of the 256 compute units. A chunk of a 256 x 256 tile
 // takes 1.55 us, which is the rate of a large library product without group
 // scales; what is lost is the last round and 7 us of start and end per tile. One
-// row, 10240 x 1280: 4.8 us for 13 MB. 24 x 3072 x 12288: 10.7 us the tiles of 16
-// slices (3.5 TB/s) and 3 us their sums. 1023 x 1283 x 1272 to fp32: 15 us, of which
+// row, 10240 x 1280: 4.8 us for 13 MB. 24 x 3072 x 12288: 10 to 11 us the tiles of 16
+// slices (3.5 TB/s) and 2 to 4 us their sums. 1023 x 1283 x 1272 to fp32: 15 us, of which
 // 7 are a launch, a tile's start and its end, the rest 10 chunks of 0.65 us that
 // wait for their copies and LDS reads (without the widening 0.55).
 #include <hip/hip_runtime.h>
@@ -614,8 +615,6 @@ struct GemmPlan {
 // The variant and the split along K of least estimated time. A round of tiles
 // that leaves slots empty runs its chunks the faster. A split costs a second
 // launch and the partial tiles written and read, about 7 us and 2.5 TB/s.
-// Against the best of all variants on 24 shapes from 65 x 3072 x 3072 to
-// 4608 x 12288 x 3072 the choice is within 4% on 22 and 12% on the others.
 template <int COUNT>
 GemmPlan least(const TileCost (&tiles)[COUNT], int64_t M, int64_t N, int64_t Kp, bool split) {
   const int C = static_cast<int>(Kp / kChunk), cus = resident_slots() / 2;

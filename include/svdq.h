@@ -704,8 +704,10 @@ size_t svdq_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t Kp);
  * sum_{k in g} a[m][k] * w[n][k] + bias[n]). Y is f16, bf16 or f32; bias is N
  * fp32 values or NULL. Codes 16-byte aligned, Kp a multiple of 128 up to 2^22.
  * Sums across groups are fp32. For f16 and bf16 outputs the sum inside a group
- * is the 8-bit matrix instruction's (relative error 1e-5 to 5e-5, below the
- * output's rounding); for f32 outputs it is exact to fp32 rounding. ws: NULL or
+ * is the 8-bit matrix instruction's, which aligns the products to their largest: it
+ * may be off by 2^-11 of the group's largest |a * w| (times the scales; 2^-13
+ * measured), which exceeds the output's rounding where a group's products cancel.
+ * For f32 outputs it is exact to fp32 rounding. ws: NULL or
  * a 16-byte aligned workspace; with at least svdq_gemm_fp8_workspace_bytes
  * bytes a shape with few tiles and long K is split along K. */
 int svdq_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
