@@ -1172,35 +1172,24 @@ def attention(Q, K, V, Out, scale: float | None = None, softcap: float = 0.0, sl
         check(status, "svdq_attention")
 
 
-def _capturing(device) -> bool:
-    return device.type == "cuda" and _torch().cuda.is_current_stream_capturing()
-
-
 class _Buffers:
     """Flat buffers kept between calls by name and type, replaced when a larger one is
-    needed. A buffer that a graph capture has used is never given back: the graph's
-    replays write there. Another goes back behind the work queued on the stream that
-    outgrew it, which may not be the one it was allocated on."""
+    needed. The smaller ones stay: the replays of a graph captured before write there,
+    and work on another stream may be queued on them. Each is at least twice the one
+    before, so all those outgrown together take no more than the one in use."""
 
     def __init__(self, device):
         self.device = device
         self.kept = {}
-        self.captured = set()          # keys of kept buffers that a capture has used
-        self.outgrown = []             # such buffers, after a larger one took their place
+        self.outgrown = []
 
-    def get(self, name, count, dtype, stream=None):
-        """At least `count` elements, for work on the given or the current stream."""
-        key = name, dtype
-        t = self.kept.get(key)
-        if t is None or t.numel() < count:
-            if key in self.captured:
-                self.outgrown.append(t)
-                self.captured.remove(key)
-            elif t is not None and t.is_cuda:
-                t.record_stream(stream or _torch().cuda.current_stream(t.device))
-            t = self.kept[key] = _torch().empty(count, dtype=dtype, device=self.device)
-        if _capturing(self.device):
-            self.captured.add(key)
+    def larger(self, name, count, dtype):
+        """A new buffer of `count` elements at least, in place of the one kept, if any."""
+        t = self.kept.get((name, dtype))
+        if t is not None:
+            self.outgrown.append(t)
+            count = max(count, 2 * t.numel())
+        t = self.kept[name, dtype] = _torch().empty(count, dtype=dtype, device=self.device)
         return t
 
 
@@ -1212,7 +1201,7 @@ class Linear:
     svdq_linear_tiled; a prep of fmt "fp8" runs svdq_linear_fp8) on the current stream and
     returns Y (M x N, ``out_dtype``), optionally through the fused activation
     (``"gelu_tanh"``). The workspace is kept between calls and grown when a
-    larger M arrives; one that a graph capture has used stays for its replays."""
+    larger M arrives; the smaller ones stay, for graphs captured with them."""
 
     def __init__(self, prep: Prepared, bias: Optional[np.ndarray] = None, device="cuda",
                  out_dtype=None, activation=None, tiled: bool = False):
@@ -1250,9 +1239,9 @@ class Linear:
         self.activation = activation
         self.device = dev
         self._buffers = _Buffers(dev)
+        self.ws = None
 
-    def workspace(self, M: int, stream=None):
-        """The kept workspace, of M rows at least, for work on the given or the current stream."""
+    def workspace(self, M: int):
         torch = _torch()
         if self.fmt == "w4a16":
             need = w4a16_x_tiled_bytes(M, self.K)
@@ -1266,7 +1255,9 @@ class Linear:
                     + gemm_tiled_workspace_bytes(M, self.N, self.K))
         else:
             need = linear_workspace_bytes(M, self.K, self.R)
-        return self._buffers.get("ws", need, torch.uint8, stream)
+        if self.ws is None or self.ws.numel() < need:
+            self.ws = self._buffers.larger("ws", need, torch.uint8)
+        return self.ws
 
     def __call__(self, X, Y=None, stream=None):
         torch = _torch()
@@ -1280,16 +1271,15 @@ class Linear:
         if self.fmt == "w4a16":
             if self.activation is not None:
                 raise ValueError("the weight-only baseline has no fused activation")
-            linear_w4a16(X, self.w_codes, self.w_scales, self.bias, Y,
-                         self.workspace(M, stream), stream)
+            linear_w4a16(X, self.w_codes, self.w_scales, self.bias, Y, self.workspace(M), stream)
             return Y
         if self.fmt == "fp8":
-            linear_fp8(X, self.w_codes, self.w_scales, self.bias, Y, self.workspace(M, stream),
-                       stream, self.activation)
+            linear_fp8(X, self.w_codes, self.w_scales, self.bias, Y, self.workspace(M), stream,
+                       self.activation)
             return Y
         run = linear_mx if self.fmt == "mxfp4" else linear_tiled if self.tiled else linear
         run(X, self.inv_smooth, self.L1p, self.L2t, self.R, self.w_codes, self.w_scales,
-            self.bias, Y, self.workspace(M, stream), stream, self.activation)
+            self.bias, Y, self.workspace(M), stream, self.activation)
         return Y
 
 
@@ -1324,7 +1314,7 @@ class Conv2d:
         if Y is None:
             Y = torch.empty((B, OH, OW, lin.N), dtype=lin.out_dtype or X.dtype,
                             device=lin.device)
-        ws = lin.workspace(max(B * OH * OW, 1), stream)
+        ws = lin.workspace(max(B * OH * OW, 1))
         run = conv2d_mx if lin.fmt == "mxfp4" else conv2d_tiled if lin.tiled else conv2d
         run(X, self.KH, self.KW, self.stride, self.pad, lin.inv_smooth, lin.L1p, lin.L2t, lin.R,
             lin.w_codes, lin.w_scales, lin.bias, Y, ws, stream, lin.activation)

@@ -34,14 +34,13 @@ class KeyValueCache:
         shape = (batch, capacity, kv_heads, head_dim)
         self.k = torch.empty(shape, dtype=dtype, device=device)
         self.v = torch.empty(shape, dtype=dtype, device=device)
+        self.capacity = capacity
         self.length = 0
 
-    def append(self, k, v):
-        """Take in k and v (batch x tokens x kv_heads x head_dim, the cache's type); the
-        views of all tokens held. What does not fit is refused before anything changes."""
-        torch = api._torch()
+    def _refuse(self, k, v):
+        """Raises for the first of k and v that the cache does not take."""
         for name, t in (("k", k), ("v", v)):
-            if not isinstance(t, torch.Tensor):
+            if not isinstance(t, api._torch().Tensor):
                 raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
             want = (self.k.shape[0], k.shape[1] if k.dim() == 4 else None, *self.k.shape[2:])
             if tuple(t.shape) != want:
@@ -49,9 +48,23 @@ class KeyValueCache:
             if t.dtype != self.k.dtype or t.device != self.k.device:
                 raise ValueError(f"{name}: {t.dtype} on {t.device}, the cache holds {self.k.dtype} "
                                  f"on {self.k.device}")
-        end = self.length + k.shape[1]
-        if end > self.k.shape[1]:
-            raise ValueError(f"cache of {self.k.shape[1]} tokens: {end} needed")
+
+    def append(self, k, v):
+        """Take in k and v (batch x tokens x kv_heads x head_dim, the cache's type); the
+        views of all tokens held. What does not fit is refused before anything changes."""
+        held = self.k
+        try:
+            b, n, h, d = k.shape
+            good = ((b, self.capacity, h, d) == held.shape and v.shape == k.shape
+                    and k.dtype is held.dtype and v.dtype is held.dtype
+                    and k.device == held.device and v.device == held.device)
+        except (AttributeError, TypeError, ValueError):
+            good = False
+        if not good:
+            self._refuse(k, v)
+        end = self.length + n
+        if end > self.capacity:
+            raise ValueError(f"cache of {self.capacity} tokens: {end} needed")
         self.k[:, self.length:end].copy_(k)
         self.v[:, self.length:end].copy_(v)
         self.length = end
@@ -67,8 +80,8 @@ class AttentionBlock:
     block's output and X + residual, which are the next block's X and residual.
     With a KeyValueCache the tokens are appended to it and attend to all that it
     holds; a call that raises leaves the cache's length as it was. Buffers are kept between calls and grown when more tokens arrive, so
-    one block serves one stream at a time (those that a graph capture has used stay
-    for its replays), and Y and h are new tensors."""
+    one block serves one stream at a time (the smaller ones stay, for graphs captured
+    with them), and Y and h are new tensors."""
 
     def __init__(self, gain, qkv, out, heads: int, kv_heads: int, head_dim: int,
                  qkv_bias=None, out_bias=None, eps: float = 1e-6, softcap: float = 0.0,
@@ -107,7 +120,10 @@ class AttentionBlock:
     def _buffer(self, name, shape, dtype):
         """The buffer kept under `name`, as a tensor of this shape."""
         count = math.prod(shape)
-        return self._buffers.get(name, count, dtype)[:count].view(shape)
+        t = self._kept.get((name, dtype))
+        if t is None or t.numel() < count:
+            t = self._buffers.larger(name, count, dtype)
+        return t[:count].view(shape)
 
     def _codes(self, name, M, K):
         torch = api._torch()

@@ -120,26 +120,20 @@ def test_vectors_of_another_length(over):
         sq.AttentionBlock(qkv=qkv, out=out, heads=4, kv_heads=2, head_dim=32, device="cpu", **a)
 
 
-def kept_by(thing):
-    """Addresses of all buffers that a layer or block holds."""
-    b = thing._buffers
-    return {t.data_ptr() for t in (*b.kept.values(), *b.outgrown)}
-
-
-def test_buffers_of_a_capture_outlive_larger_calls(monkeypatch):
+def test_buffers_of_smaller_calls_outlive_larger_ones(monkeypatch):
     """A graph's replays write to the buffers of its capture: a later, larger call may
-    not give them back. Those of eager calls it does."""
+    not give them back. All that are outgrown take no more than those in use."""
+    for f in ("rmsnorm_quantize_fp8", "gemm_fp8", "quantize_act_fp8", "attention", "linear_fp8"):
+        monkeypatch.setattr(block_module.api, f, lambda *a, **k: None)
     block = sq.AttentionBlock(np.ones(256, np.float32), *weights(), 4, 2, 32, device="cpu")
     lin = sq.Linear(sq.prepare_weights_fp8(np.ones((256, 256), np.float32)), device="cpu")
-    take = {block: lambda n: block._buffer("o", (n,), torch.float16), lin: lambda n: lin.workspace(n)}
-    for thing, get in take.items():
-        monkeypatch.setattr(block_module.api, "_capturing", lambda device: False)
-        get(64)
-        eager = kept_by(thing)
-        monkeypatch.setattr(block_module.api, "_capturing", lambda device: True)
-        graph = get(128).data_ptr()
-        assert thing._buffers.outgrown == [] and kept_by(thing) == {graph} != eager
-        monkeypatch.setattr(block_module.api, "_capturing", lambda device: False)
-        larger = [get(n).data_ptr() for n in (256, 512)]
-        assert get(100).data_ptr() == larger[1]
-        assert kept_by(thing) == {graph, larger[1]}
+    for thing, rank in ((block, 3), (lin, 2)):
+        b, addresses = thing._buffers, set()
+        for n in (8, 9, 10, 64, 100, 101, 1000):
+            thing(torch.zeros((1, n, 256)[3 - rank:], dtype=torch.float16))
+            addresses |= {t.data_ptr() for t in b.kept.values()}
+        assert addresses == {t.data_ptr() for t in (*b.kept.values(), *b.outgrown)}
+        assert sum(t.nbytes for t in b.outgrown) <= sum(t.nbytes for t in b.kept.values())
+        kept = dict(b.kept)
+        thing(torch.zeros((1, 500, 256)[3 - rank:], dtype=torch.float16))
+        assert all(b.kept[k] is t for k, t in kept.items())
