@@ -31,7 +31,7 @@ lib = C.CDLL(LIB_PATH)
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_DTYPE, ERR_RANK, ERR_WORKSPACE, ERR_HIP, \
     ERR_NO_DEVICE, ERR_INTERNAL, ERR_GROUP, ERR_ACT = range(12)
 ACT_NONE, ACT_GELU_TANH = 0, 1
-F16, F32, BF16 = 1, 2, 3
+F16, F32, BF16, E4M3 = 1, 2, 3, 4
 GROUP = 64
 MX_BLOCK = 32
 FP8_BLOCK = 128
@@ -131,6 +131,17 @@ _SIGS = {
     "svdq_attention_workspace_bytes": (C.c_size_t, [_i64, _i64, _i64, _i64, _i64, _i64]),
     "svdq_attention": (_int, [_p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _p, _f, _f,
                               _p, _i32, _p, _p, _i64, _p, C.c_size_t, _p]),
+    "svdq_norm_rotary": (_int, [_p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _p, _p, _p, _i64, _f,
+                                _i32, _p, _p, _f, _p]),
+    "svdq_paged_write": (_int, [_p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _p, _p, _p, _i64, _f,
+                                _i32, _p, _p, _f, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _p, _p,
+                                _p]),
+    "svdq_paged_read": (_int, [_p, _p, _int, _i64, _i64, _i64, _i64, _p, _p, _p, _i64, _p, _i64,
+                               _i64, _i64, _i64, _p, _p, _int, _p, _p]),
+    "svdq_paged_attention_workspace_bytes": (C.c_size_t, [_i64, _i64, _i64, _i64, _i64, _i64]),
+    "svdq_paged_attention": (_int, [_p, _p, _int, _i64, _i64, _i64, _i64, _p, _p, _p, _int, _i64,
+                                    _i64, _i64, _i64, _p, _p, _p, _i64, _p, _p, _i64, _f, _f, _p,
+                                    _i32, _p, C.c_size_t, _p]),
     "svdq_clock_rates": (_int, [_p, _p]),
     "svdq_clock_probe": (_int, [_p, _i32, _i64, _p, _p]),
     "svdq_clock_mark": (_int, [_p, _p, _p]),

@@ -90,6 +90,8 @@ enum {
 /* dtype codes for X and Y. SVDQ_BF16 is taken by the 8-bit attention block's
  * entry points only; the others return SVDQ_ERR_DTYPE for it. */
 enum { SVDQ_F16 = 1, SVDQ_F32 = 2, SVDQ_BF16 = 3 };
+/* Pages of a key-value cache only: e4m3 codes. */
+enum { SVDQ_E4M3 = 4 };
 
 /* Activation applied by K2's epilogue to the fp32 result before its one
  * rounding to the output type. GELU is the tanh form between the two linears
@@ -755,6 +757,94 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
                    const int64_t* strides, float scale, float softcap, const float* slopes,
                    int32_t causal, const int32_t* prefix, const int32_t* key_ranges,
                    int64_t key_ranges_batch, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged key-value cache (not on the pages; each operator is stated by its
+ * formula). A pool holds `pages` pages of page_size tokens (a power of two, 16 ..
+ * 1024); page p lies p * page_stride bytes behind the pool's start, in it Hkv heads
+ * x page_size tokens x D channels, contiguous, of the tokens' type (f16, bf16) or as
+ * e4m3 codes (cache_dtype SVDQ_E4M3) of one fp32 scale per head, finite and above 0
+ * (k_scales, v_scales: Hkv values, NULL: 1). A token's slot is page * page_size + its
+ * place in the page. A sequence's token j lies in page tables[b][j / page_size]
+ * (tables: B x width int32). Slots, tables, lengths and starts lie on the device, so
+ * that one captured graph serves growing sequences; a slot or page outside the pool is
+ * no place at all: nothing is stored there, read from there or seen there.
+ *
+ * Tokens are rows of H heads of D channels (a multiple of 8 up to 128), contiguous
+ * channels, any token and head stride that is a multiple of 8 elements, 16-byte
+ * aligned. Page strides are multiples of 16 bytes. T, B or L = 0 is a call that
+ * does nothing.
+ */
+
+/* Device: norm and rotation of query and key heads in one pass, fp32, rounded once:
+ *   u = x / sqrt(mean(x^2) + eps) * gain   over each head (eps < 0: without; a gain is
+ *                                          D fp32 values or NULL);
+ *   pair i of `pairs` turns by the angle positions[t] * freqs[i] radians (fp64):
+ *     (a, b) <- factor * (a cos - b sin, a sin + b cos),
+ *     channels (i, i + pairs), or (2i, 2i + 1) if interleaved; channels from
+ *     2 * pairs on stay as they are. pairs = 0: no rotation.
+ * A cosine is good to 2^-22 for positions * freqs up to 2^31. strides: 8 element
+ * strides, (token, head) of Q, K, Q_out and K_out. Hq or Hkv may be 0. Q_out may be Q,
+ * and K_out K, with the same strides; outputs may not overlap the inputs otherwise. */
+int svdq_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, int dtype, int64_t T,
+                     int64_t Hq, int64_t Hkv, int64_t D, const int64_t* strides,
+                     const int32_t* positions, const double* freqs, int64_t pairs, float factor,
+                     int32_t interleaved, const float* q_gain, const float* k_gain, float eps,
+                     hipStream_t stream);
+
+/* Device: the same pass with keys (normed and rotated) and values (as they are) stored
+ * at the tokens' slots: rounded once, to the tokens' type or to the code
+ *   e4m3_rne(clamp(u * fp32(1 / scale), -448, 448)); NaN and infinities: the NaN code.
+ * A token whose slot is not in the pool (-1, say) stores nothing; its queries are
+ * written all the same. Slots in the pool must differ: where two tokens share one, any
+ * mixture of the two is stored. strides: (token, head) of Q, K, V and Q_out. Hq = 0
+ * writes keys and values alone. */
+int svdq_paged_write(const void* Q, const void* K, const void* V, void* Q_out, int dtype, int64_t T,
+                     int64_t Hq, int64_t Hkv, int64_t D, const int64_t* strides,
+                     const int32_t* positions, const double* freqs, int64_t pairs, float factor,
+                     int32_t interleaved, const float* q_gain, const float* k_gain, float eps,
+                     const int32_t* slots, void* k_pages, void* v_pages, int cache_dtype,
+                     int64_t pages, int64_t page_size, int64_t k_page_stride,
+                     int64_t v_page_stride, const float* k_scales, const float* v_scales,
+                     hipStream_t stream);
+
+/* Device: sequences back from their pages, K_out and V_out (B x L x Hkv x D) in f16 or
+ * bf16 (16-bit pages: of the same type): token j < lengths[b] of sequence b, code *
+ * scale rounded once. Rows from lengths[b] on, and of pages outside the pool, are left
+ * as they were. strides: (batch, token, head) of K_out and V_out. */
+int svdq_paged_read(const void* k_pages, const void* v_pages, int cache_dtype, int64_t pages,
+                    int64_t page_size, int64_t k_page_stride, int64_t v_page_stride,
+                    const float* k_scales, const float* v_scales, const int32_t* tables,
+                    int64_t width, const int32_t* lengths, int64_t B, int64_t L, int64_t Hkv,
+                    int64_t D, void* K_out, void* V_out, int dtype, const int64_t* strides,
+                    hipStream_t stream);
+
+/* Bytes of the partial outputs of an attention of T tokens of B sequences over up to
+ * `capacity` keys each (width * page_size) on the current device. */
+size_t svdq_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t capacity, int64_t Hq,
+                                            int64_t Hkv, int64_t D);
+
+/* Device: attention of new tokens over the cache. Sequence b's tokens are rows
+ * starts[b] .. starts[b + 1] - 1 of Q and Out (starts: B + 1 ascending int32 in 0 .. T;
+ * none, one or many tokens each) and the last of the lengths[b] tokens in its pages,
+ * its own keys among them: row i's position is lengths[b] - n + i.
+ *   x[i][j] = scale * k_scale * q_i . k_j; softcap and slopes as in svdq_attention;
+ *   out_i = v_scale * sum_j softmax_j(x[i][j]) v_j over the keys j < lengths[b] in
+ *   pages of the pool with, if causal, j <= position of i.
+ * Keys and values are the pages' values or codes. A row that sees no key is 0; a key
+ * that a row does not see does not reach its output whatever its page holds. Rows of
+ * no sequence are left as they were. strides: (token, head) of Q and Out, which may not
+ * overlap. T * Hq: up to 2^30. ws: NULL or a 16-byte aligned workspace; with at least
+ * svdq_paged_attention_workspace_bytes bytes work is split along the keys. Two calls
+ * that may run at once need a workspace each. */
+int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t Hq, int64_t Hkv,
+                         int64_t D, const int64_t* strides, const void* k_pages,
+                         const void* v_pages, int cache_dtype, int64_t pages, int64_t page_size,
+                         int64_t k_page_stride, int64_t v_page_stride, const float* k_scales,
+                         const float* v_scales, const int32_t* tables, int64_t width,
+                         const int32_t* lengths, const int32_t* starts, int64_t B, float scale,
+                         float softcap, const float* slopes, int32_t causal, void* ws,
+                         size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement utilities (not part of the method): the shader clock during a
