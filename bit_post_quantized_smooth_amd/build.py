@@ -23,7 +23,9 @@ HIP_SOURCES = ["k1_quant_down.hip", "k2_w4a4_gemm.hip", "k2_mx_gemm.hip", "k2_w4
                "k2_w4a4_tiled.hip", "gelu.hip", "lowrank_pack.hip", "clock_probe.hip",
                "abi_device.hip",
                "abi_noalloc.hip", "fp8_quant.hip", "fp8_gemm.hip", "attention.hip",
-               "abi_block.hip", "rotary_cache.hip", "paged_attention.hip", "abi_paged.hip"]
+               "abi_block.hip", "rotary_cache.hip", "paged_attention.hip",
+               "paged_attention_f16_64.hip", "paged_attention_f16_128.hip",
+               "paged_attention_bf16_64.hip", "paged_attention_bf16_128.hip", "abi_paged.hip"]
 HOST_SOURCES = {
     # the quantizer's fp32 divide/multiply must round exactly: no contraction
     "host_prep.cpp": ["-ffp-contract=off"],

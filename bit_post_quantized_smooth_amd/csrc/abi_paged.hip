@@ -7,9 +7,11 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 #include <utility>
 
 #include "../../include/svdq.h"
+#include "attention.hpp"
 #include "block_launch.hpp"
 #include "host_internal.hpp"
 #include "paged.hpp"
@@ -287,9 +289,9 @@ namespace {
 
 int check_paged_attention_sizes(const char* fn, int64_t T, int64_t B, int64_t capacity, int64_t Hq,
                                 int64_t Hkv, int64_t D) {
-  if (T < 0 || B < 0 || B > kMaxTokens || capacity < 0 || capacity > kMaxTokens || Hkv < 1 ||
-      Hkv > kMaxHeads || Hq < Hkv || Hq > kMaxHeads || Hq % Hkv != 0 || T > kMaxTokens / Hq ||
-      !paged_attention_fits(T, Hq)) {
+  if (T < 0 || B < 0 || B > kMaxTokens || capacity < 0 || capacity > kMostKeys || Hkv < 1 ||
+      Hkv > kMaxHeads || Hq < Hkv || Hq > kMaxHeads || Hq % Hkv != 0 || Hq / Hkv > kMostGroup ||
+      T > kMaxTokens / Hq) {
     set_error("%s: %lld tokens of %lld sequences, %lld keys, %lld over %lld heads out of range", fn,
               (long long)T, (long long)B, (long long)capacity, (long long)Hq, (long long)Hkv);
     return SVDQ_ERR_SHAPE;
@@ -307,7 +309,8 @@ size_t svdq_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t capaci
                                             Hq, Hkv, D);
   clear_error();                       // a size query reports by its 0 alone
   if (s != SVDQ_OK) return 0;
-  return 0;
+  const PartBytes p = paged_attention_parts(T, B, capacity, Hkv, Hq / Hkv, D);
+  return p.ml + p.o;
 }
 
 int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t Hq, int64_t Hkv,
@@ -351,8 +354,14 @@ int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t
   g.lengths = lengths;
   g.starts = starts;
   g.slopes = slopes;
-  g.scale = scale;
-  g.softcap = softcap;
+  constexpr float kLog2e = 1.4426950408889634f;
+  g.q_sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
+  g.scale2 = g.q_sign != 0 ? std::fabs(scale) * kLog2e : 1.f;
+  // finite at any cap: a score of 0 times an infinity would be NaN
+  constexpr float kMost = std::numeric_limits<float>::max();
+  g.cap = softcap == 0.f ? kNoCap : softcap <= kNearest ? kNearCap : kAnyCap;
+  g.cap_in = softcap > 0.f ? std::fmin(2.0f * kLog2e * (std::fabs(scale) / softcap), kMost) : 0.f;
+  g.cap2 = std::fmin(softcap * kLog2e, kMost);
   g.causal = causal != 0;
   g.width = static_cast<int>(width);
   g.B = static_cast<int>(B);
@@ -361,7 +370,12 @@ int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t
   g.G = static_cast<int>(Hq / Hkv);
   g.D = static_cast<int>(D);
   g.capacity = static_cast<int>(capacity);
-  (void)ws_bytes;
+  const PartBytes parts = paged_attention_parts(T, B, capacity, Hkv, Hq / Hkv, D);
+  if (parts.o > 0 && ws != nullptr && ws_bytes >= parts.ml + parts.o) {
+    g.part_rows = T * (Hq / Hkv) <= 32 ? 32 : 128;
+    g.part_ml = static_cast<float*>(ws);
+    g.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + parts.ml);
+  }
   return check_hip(launch_paged_attention(g, dtype, stream), fn);
 }
 

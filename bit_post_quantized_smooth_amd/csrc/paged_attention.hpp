@@ -20,13 +20,33 @@ struct PagedArgs {
   const int32_t* lengths;    // B: tokens of each sequence in the cache
   const int32_t* starts;     // B + 1: each sequence's first token among the T
   const float* slopes;       // per query head, or null
-  float scale, softcap;
+  float* part_ml;            // parts: maximum and sum per row
+  float* part_o;             // parts: unnormalized outputs, D per row
+  // as in AttnArgs, without the head's scale
+  int q_sign;
+  float scale2;
+  int cap;
+  float cap_in, cap2;
   int causal;
   int width, B, T, Hkv, G, D;
   int capacity;              // width << page_log2
+  int part_rows;             // rows of a part; 0: tiles are not split
 };
 
-bool paged_attention_fits(int64_t T, int64_t Hq);
-hipError_t launch_paged_attention(const PagedArgs& g, int dtype, hipStream_t stream);
+// Largest group of query heads, and most keys of a sequence: their products with
+// 2^30 rows fit the 64 bits that work is counted in.
+constexpr int64_t kMostGroup = 256;
+constexpr int64_t kMostKeys = int64_t{1} << 26;
+
+// Bytes of the parts' maxima and sums, and of their outputs, on the current device.
+struct PartBytes {
+  size_t ml, o;
+};
+PartBytes paged_attention_parts(int64_t T, int64_t B, int64_t capacity, int64_t Hkv, int64_t G,
+                                int64_t D);
+// The kernel of heads of up to DP channels (64 or 128); a source file each.
+template <class T, int DP>
+void launch_paged_tiles(const PagedArgs& g, unsigned grid, hipStream_t stream);
+hipError_t launch_paged_attention(PagedArgs g, int dtype, hipStream_t stream);
 
 }  // namespace svdq

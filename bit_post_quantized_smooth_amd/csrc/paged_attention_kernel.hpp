@@ -1,0 +1,589 @@
+// Attention of new tokens over a paged cache (gfx950).
+//
+//   x_ij = scale * s_k * q_i . k_j;  with a cap: x_ij = cap * tanh(x_ij / cap);
+//   with slopes: x_ij -= slope_h * |pos_i - j|;
+//   o_i = s_v * sum_j exp(x_ij) v_j / sum_j exp(x_ij) over the keys j that row i sees:
+//   j < length of its sequence, in a page of the pool, and, if causal, j <= pos_i,
+//   where the sequence's n new tokens are its last: pos_i = length - n + i.
+// s_k and s_v are the head's scales of e4m3 codes (1 of 16-bit pages): s_k is part of
+// the scores' scale and s_v of the division by the weights' sum, so that codes enter
+// the products as they are (every one is exact in fp16 and bf16).
+//
+// The softmax in one pass, its roundings and the matrix products are those of
+// attention_core.hpp: a wave owns 32 rows (query and head of one key head) and its
+// tiles of K and V lie in LDS as 16-bit values.
+//
+// Two kinds of row tiles, by a sequence's own rows, in one launch, so that single
+// tokens and chunks of prompts run side by side:
+//   up to 32 rows (single tokens): the waves of a workgroup take blocks of 32 keys in
+//   turn. Each has its own part of LDS and fetches the next block into registers before
+//   it works on one (64 KB of codes in flight per compute unit, or 128 KB), with no
+//   barrier until the four add up their outputs at the end;
+//   more rows: 128 per workgroup, 32 a wave, sharing tiles of 64 keys in two stages;
+//   16-bit tiles go straight into LDS, codes through registers, widened on the way.
+//
+// The lengths are only known on the device. So the tiles, over all sequences and key
+// heads, are laid end to end by an estimate of their work, and each workgroup of a
+// fixed number, as many as are resident, takes an equal share of the line: the shares
+// balance whatever the lengths are. Where a share's border falls into a tile the keys
+// are split there, each part writes fp32 outputs with their maxima and sums, and a
+// second kernel joins them in order. Tiles of little work are left whole.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/svdq.h"
+#include "attention_core.hpp"
+#include "block_common.hpp"
+#include "k2_common.hpp"
+#include "paged_attention.hpp"
+#include "paged_line.hpp"
+
+namespace svdq {
+
+namespace {
+
+// Page numbers of 64 groups of 16 keys, one a lane, and of the 64 behind them, which are
+// on their way while these are used. -1: not in the pool.
+struct PageWindow {
+  const PagedArgs* g;
+  const int32_t* table;
+  int at, now, then;
+  uint64_t there;
+
+  __device__ __forceinline__ int fetch(int group) const {
+    const int i = (group + static_cast<int>(threadIdx.x & 63)) >> (g->pages.page_log2 - 4);
+    if (i >= g->width) return -1;
+    return table[i];
+  }
+  __device__ __forceinline__ void begin(const PagedArgs& args, int b, int group) {
+    g = &args;
+    table = args.tables + static_cast<int64_t>(b) * args.width;
+    at = group & ~63;
+    now = fetch(at);
+    then = fetch(at + 64);
+    see();
+  }
+  __device__ __forceinline__ void see() {
+    there = __builtin_amdgcn_ballot_w64(now >= 0 && now < g->pages.count);
+  }
+  // Groups are asked for in ascending order.
+  __device__ __forceinline__ void seek(int group) {
+    while (group - at >= 64) {
+      now = then;
+      at += 64;
+      then = fetch(at + 64);
+      see();
+    }
+  }
+  __device__ __forceinline__ bool has(int group) const { return there >> (group - at) & 1; }
+  __device__ __forceinline__ int page(int group) const {
+    return __builtin_amdgcn_readlane(now, group - at);
+  }
+};
+
+struct Scores {
+  float scale2, cap_in, cap2;
+};
+
+// What the two kinds of tiles share. CODED: pages of e4m3 codes.
+template <class T, int DP, int RW, int CAP, bool SLOPES, bool CODED>
+struct PagedTile : AttentionCore<T, DP, RW, CAP, SLOPES, 128, Scores, true> {
+  typedef AttentionCore<T, DP, RW, CAP, SLOPES, 128, Scores, true> Core;
+  using typename Core::Lds;
+  using typename Core::vec;
+  using Core::DB, Core::DS, Core::KB, Core::KT, Core::UNITS;
+  using Core::g, Core::lds, Core::lane, Core::wave, Core::rl, Core::h, Core::qf, Core::o, Core::m,
+      Core::l, Core::lo, Core::pos, Core::width, Core::large, Core::w_lo, Core::w_hi,
+      Core::w_lo_max, Core::w_hi_min, Core::slope2, Core::kb0, Core::vb0, Core::holes;
+  static constexpr int ESIZE = CODED ? 1 : 2;
+  static constexpr int LPR = DP * ESIZE / 16;       // lanes that fetch a row
+  static constexpr int RPI = 64 / LPR;              // rows of one fetch of a wave
+
+  const PagedArgs& a;
+  PageWindow pages;
+  int hk, b, last;                                  // last: keys that any row of the tile sees
+  float vscale;
+  // the lane's share of a fetch: its place in the rows (beyond any buffer past D) and in LDS
+  uint32_t fetch_at;
+  int put_at;
+
+  __device__ __forceinline__ PagedTile(const PagedArgs& args, const Scores& scores, Lds& shared)
+      : Core(scores, shared), a(args) {}
+
+  // Rows 16 * group .. of K or V: base and bytes; none of a page outside the pool.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const void* pool, int64_t stride, int group) const {
+    const int key = group * kGroupKeys;
+    const int in_page = key & ((1 << a.pages.page_log2) - 1);
+    const int n = min(last - key, kGroupKeys);
+    const bool there = n > 0 && pages.has(group);
+    const int64_t page = there ? pages.page(group) : 0;
+    const char* base = static_cast<const char*>(pool) + page * stride +
+                       ((static_cast<int64_t>(hk) << a.pages.page_log2) + in_page) * a.D * ESIZE;
+    return make_buffer(base, there ? static_cast<uint32_t>(n * a.D * ESIZE) : 0u);
+  }
+
+  // 16 codes or 8 values a lane, of RPI rows from row `row0` of the group on
+  __device__ __forceinline__ v4i fetch(__amdgpu_buffer_rsrc_t buf, int row0) const {
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                       buf, static_cast<int>(fetch_at), row0 * a.D * ESIZE, 0));
+  }
+  // The same into LDS rows from `to` on (16-byte units from its start; row `row0` of them),
+  // widened. The twist of a row is the exclusive or of its bits' twists, and a fetch's
+  // rows lie within RPI: one address per lane, a constant each.
+  __device__ __forceinline__ void put(uint8_t* to, int row0, v4i x) const {
+    uint8_t* p = to + row0 * DP * 2 + (put_at ^ (Core::twist(row0) * 16));
+    if constexpr (CODED) {
+      v4i w[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int word = x[i];
+        w[i >> 1][2 * (i & 1)] = widen<false>(word);
+        w[i >> 1][2 * (i & 1) + 1] = widen<true>(word);
+      }
+      // the second 8 may lie behind D: the next row's
+      if (16 * (lane % LPR) + 8 >= a.D) w[1] = v4i{0, 0, 0, 0};
+      *reinterpret_cast<v4i*>(p) = w[0];
+      *reinterpret_cast<v4i*>(to + row0 * DP * 2 + (put_at ^ ((Core::twist(row0) ^ 1) * 16))) = w[1];
+    } else {
+      *reinterpret_cast<v4i*>(p) = x;
+    }
+  }
+  template <bool HIGH>
+  static __device__ __forceinline__ int widen(int word) {
+    if constexpr (__is_same(T, _Float16))
+      return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, HIGH));
+    else
+      return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, 1.0f, HIGH));
+  }
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+    m = kNegInf;
+    l = 0.f;
+    large = false;
+  }
+
+  // The lane's row r of sequence s: what it sees, its slope, its queries.
+  __device__ __forceinline__ void rows_of(const Sequence& s, const Place& p, int r) {
+    lane = Core::opaque(threadIdx.x & 63);   // nothing of a lane's is kept from tile to tile
+    wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    rl = lane & 31;
+    h = lane >> 5;
+    hk = p.hk;
+    b = p.b;
+    holes = 0;
+    vscale = a.pages.v_scales != nullptr ? a.pages.v_scales[hk] : 1.f;
+    fetch_at = 16 * (lane % LPR) < a.D * ESIZE
+                   ? static_cast<uint32_t>((lane / LPR) * a.D * ESIZE + 16 * (lane % LPR))
+                   : 0x80000000u;
+    const int row = lane / LPR;
+    put_at = row * DP * 2 + (((CODED ? 2 : 1) * (lane % LPR)) ^ Core::twist(row)) * 16;
+    kb0 = Core::k_base();
+    vb0 = Core::v_base();
+    const bool real = r < s.n * a.G;
+    const int i = real ? r / a.G : 0;
+    const int head = hk * a.G + (real ? r % a.G : 0);
+    pos = s.length - s.n + i;
+    slope2 = SLOPES ? a.slopes[head] * kLog2e : 0.f;
+    const int hi = a.causal ? min(s.length, pos + 1) : s.length;
+    lo = 0;
+    width = real && hi > 0 ? static_cast<uint32_t>(hi) : 0u;
+    const T* qp = static_cast<const T*>(a.q) + (s.first + static_cast<int64_t>(i)) * a.q_t + head * a.q_h;
+#pragma unroll
+    for (int t = 0; t < DS; ++t) {
+      const int c = (2 * t + h) * 8;
+      v4i z = v4i{0, 0, 0, 0};
+      if (real && c < a.D && a.q_sign != 0) {
+        z = *reinterpret_cast<const v4i*>(qp + c);
+        if (a.q_sign < 0) z = z ^ static_cast<int>(0x80008000u);
+      }
+      qf[t] = __builtin_bit_cast(vec, z);
+    }
+  }
+  // The keys that any of the tile's rows sees.
+  __device__ __forceinline__ void last_of(const Sequence& s, int r, int rows) {
+    const int top = min(s.n, ((r + 1) * rows + a.G - 1) / a.G);     // queries before its end
+    last = a.causal ? max(0, min(s.length, s.length - s.n + top)) : s.length;
+  }
+
+  __device__ __forceinline__ bool not_finite() const {
+    bool odd = false;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) odd |= !(fabsf(o[d][e]) < __builtin_inff());
+    return __builtin_amdgcn_ballot_w64(odd) != 0;
+  }
+
+  // Output block d of row r: the outputs, or the part `slot`.
+  __device__ __forceinline__ void store(const Sequence& s, int r, int in_tile, int slot, int d, const v16f& od) {
+    if (r >= s.n * a.G) return;
+    if (slot >= 0) {
+      const int64_t row = static_cast<int64_t>(slot) * a.part_rows + in_tile;
+      if (h == 0 && d == 0) {
+        a.part_ml[2 * row] = m;
+        a.part_ml[2 * row + 1] = l;
+      }
+      if (l == 0.f) return;              // the join reads no outputs of such a row
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int ch = 32 * d + 8 * e + 4 * h;
+        if (ch < a.D)
+          *reinterpret_cast<v4f*>(a.part_o + row * a.D + ch) =
+              v4f{od[4 * e], od[4 * e + 1], od[4 * e + 2], od[4 * e + 3]};
+      }
+      return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    T* op = static_cast<T*>(a.out) + (s.first + static_cast<int64_t>(r / a.G)) * a.o_t +
+            (hk * a.G + r % a.G) * a.o_h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int ch = 32 * d + 8 * e + 4 * h;
+      if (ch < a.D) {
+        typedef T vec4 __attribute__((ext_vector_type(4)));
+        vec4 y;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = static_cast<T>(od[4 * e + c] * inv * vscale);
+        *reinterpret_cast<vec4*>(op + ch) = y;
+      }
+    }
+  }
+};
+
+// Up to 32 rows: blocks of 32 keys, a wave's own.
+template <class T, int DP, int CAP, bool SLOPES, bool CODED>
+struct FewRows : PagedTile<T, DP, 1, CAP, SLOPES, CODED> {
+  typedef PagedTile<T, DP, 1, CAP, SLOPES, CODED> Tile;
+  using Tile::a, Tile::lds, Tile::wave, Tile::lane, Tile::rl, Tile::h, Tile::o, Tile::m, Tile::l,
+      Tile::last, Tile::holes, Tile::pages, Tile::DB, Tile::RPI;
+  static constexpr int NF = 32 / RPI;               // fetches of a block and operand
+
+  struct Ahead {
+    v4i k[NF], v[NF];
+    uint32_t gone;
+  };
+
+  __device__ __forceinline__ FewRows(const PagedArgs& args, const Scores& scores, typename Tile::Lds& shared)
+      : Tile(args, scores, shared) {}
+
+  __device__ __forceinline__ void get(Ahead& x, int block) {
+    pages.seek(2 * block);
+    x.gone = 0;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int group = 2 * block + half;
+      const auto kb = Tile::rows(a.pages.k, a.pages.k_stride, group);
+      const auto vb = Tile::rows(a.pages.v, a.pages.v_stride, group);
+      if (!pages.has(group)) x.gone |= 1u << half;
+#pragma unroll
+      for (int i = 0; i < NF / 2; ++i) {
+        x.k[half * (NF / 2) + i] = Tile::fetch(kb, i * RPI);
+        x.v[half * (NF / 2) + i] = Tile::fetch(vb, i * RPI);
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const Ahead& x) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      Tile::put(&lds.k[32 * wave][0], i * RPI, x.k[i]);
+      Tile::put(&lds.v[32 * wave][0], i * RPI, x.v[i]);
+    }
+    holes = x.gone;
+  }
+
+  template <bool CAREFUL>
+  __device__ __forceinline__ void pass(int block0, int block1) {
+    Tile::zero();
+    int i = block0 + wave;
+    if (i >= block1) return;
+    pages.begin(a, Tile::b, 2 * i);
+    Ahead x;
+    get(x, i);
+    for (; i < block1; i += kWaves) {
+      set(x);
+      if (i + kWaves < block1) get(x, i + kWaves);
+      this->template block<CAREFUL>(0, 32 * wave, 32 * i);
+    }
+  }
+
+  __device__ __forceinline__ void run(const Sequence& s, const Place& p, int64_t x0, int64_t x1,
+                                      int64_t cost, int slot) {
+    Tile::rows_of(s, p, Tile::opaque(threadIdx.x & 31));
+    Tile::last_of(s, p.r, kFew);
+    const int blocks = (last + 31) / 32;
+    const int b0 = slot < 0 ? 0 : static_cast<int>(blocks * x0 / cost);
+    const int b1 = slot < 0 ? blocks : static_cast<int>(blocks * x1 / cost);
+    pass<false>(b0, b1);
+    if (Tile::not_finite()) pass<true>(b0, b1);
+    l = half_sum(l);
+    join(s, slot);
+  }
+
+  // Adds the waves' outputs in wave order, scaled to the common maximum: output block d
+  // by wave d.
+  __device__ __forceinline__ void join(const Sequence& s, int slot) {
+    float* mem = reinterpret_cast<float*>(&lds);
+    float* ml = reinterpret_cast<float*>(&lds + 1);
+    __syncthreads();                     // the tiles are no longer read
+    if (h == 0) {
+      ml[(wave * 32 + rl) * 2] = m;
+      ml[(wave * 32 + rl) * 2 + 1] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mem[((wave * DB + d) * 16 + e) * 64 + lane] = o[d][e];
+    __syncthreads();
+    if (wave < DB) {
+      float top = kNegInf;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml[(w * 32 + rl) * 2]);
+      // two above the largest: the sum of four finite partial outputs is finite
+      const float base = top == kNegInf ? 0.f : top + 2.f;
+      float f[kWaves];
+      l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        f[w] = __builtin_amdgcn_exp2f(ml[(w * 32 + rl) * 2] - base);
+        l = __builtin_fmaf(ml[(w * 32 + rl) * 2 + 1], f[w], l);
+      }
+      m = top == kNegInf ? top : base;
+      v16f sum;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+          v = __builtin_fmaf(mem[((w * DB + wave) * 16 + e) * 64 + lane], f[w], v);
+        sum[e] = v;
+      }
+      Tile::store(s, rl, rl, slot, wave, sum);
+    }
+    __syncthreads();                     // the next tile's rows may come
+  }
+};
+
+// 128 rows, 32 a wave: tiles of 64 keys for all, in two stages.
+template <class T, int DP, int CAP, bool SLOPES, bool CODED>
+struct ManyRows : PagedTile<T, DP, 4, CAP, SLOPES, CODED> {
+  typedef PagedTile<T, DP, 4, CAP, SLOPES, CODED> Tile;
+  using Tile::a, Tile::lds, Tile::wave, Tile::lane, Tile::rl, Tile::h, Tile::o, Tile::m, Tile::l,
+      Tile::last, Tile::holes, Tile::pages, Tile::DB, Tile::RPI, Tile::KT, Tile::width, Tile::LPR;
+  static constexpr int NF = 16 / RPI;               // fetches of a wave, tile and operand
+  v4i kx[CODED ? NF : 1], vx[CODED ? NF : 1];
+  uint32_t copy_at[CODED ? 1 : NF];
+  uint32_t gone;                                    // the next tile's holes
+  int hi, hi_min;                                   // keys that a row, all rows of the wave see
+
+  __device__ __forceinline__ ManyRows(const PagedArgs& args, const Scores& scores, typename Tile::Lds& shared)
+      : Tile(args, scores, shared) {}
+
+  // Tile t's 16 rows of this wave: on their way into registers (codes) or stage s.
+  __device__ __forceinline__ void get(int t, int s) {
+    const int group = t * (KT / kGroupKeys) + wave;
+    pages.seek(t * (KT / kGroupKeys));
+    gone = 0xFu & ~static_cast<uint32_t>(pages.there >> (t * (KT / kGroupKeys) - pages.at));
+    const auto kb = Tile::rows(a.pages.k, a.pages.k_stride, group);
+    const auto vb = Tile::rows(a.pages.v, a.pages.v_stride, group);
+    if constexpr (CODED) {
+#pragma unroll
+      for (int i = 0; i < NF; ++i) kx[i] = Tile::fetch(kb, i * RPI);
+#pragma unroll
+      for (int i = 0; i < NF; ++i) vx[i] = Tile::fetch(vb, i * RPI);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+        buffer_to_lds16(kb, &lds.k[s * KT + 16 * wave + i * RPI][0], copy_at[i],
+                        static_cast<uint32_t>(i * RPI * a.D * 2));
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+        buffer_to_lds16(vb, &lds.v[s * KT + 16 * wave + i * RPI][0], copy_at[i],
+                        static_cast<uint32_t>(i * RPI * a.D * 2));
+    }
+  }
+  __device__ __forceinline__ void set(int s) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      Tile::put(&lds.k[s * KT + 16 * wave][0], i * RPI, kx[i]);
+      Tile::put(&lds.v[s * KT + 16 * wave][0], i * RPI, vx[i]);
+    }
+  }
+
+  template <bool CAREFUL>
+  __device__ __forceinline__ void pass(int t0, int t1) {
+    Tile::zero();
+    pages.begin(a, Tile::b, t0 * (KT / kGroupKeys));
+    get(t0, 0);
+    uint32_t now = gone;
+    if constexpr (CODED) {
+      set(0);
+      if (t0 + 1 < t1) get(t0 + 1, 1);
+    }
+    // The wave sees nothing from tile `off` on; all its rows see all keys of the tiles
+    // before `out`, but for pages that are missing: from the first of those on every
+    // tile is masked. A loop for each, as one with branches would copy the outputs.
+    const int off = max(t0, min(t1, (hi + KT - 1) / KT)), out = CAREFUL ? t0 : max(t0, min(off, hi_min / KT));
+    int t = t0;
+    auto begin = [&]() {
+      const int s = (t - t0) & 1;
+      if constexpr (CODED) {
+        __syncthreads();                 // the tile is in stage s, stage s ^ 1 is free
+        holes = now;
+        if (t + 1 < t1) {
+          now = gone;
+          set(s ^ 1);
+          if (t + 2 < t1) get(t + 2, s);
+        }
+      } else {
+        __builtin_amdgcn_s_waitcnt(wait_vmem(0));
+        __syncthreads();
+        holes = now;
+        if (t + 1 < t1) {
+          get(t + 1, s ^ 1);
+          now = gone;
+        }
+      }
+      return s;
+    };
+    auto masked = [&]() {
+      const int s = begin();
+      if constexpr (!CAREFUL) {
+        this->template pair<true>(s, 0, t * KT);
+      } else {
+        const uint32_t both = holes;
+#pragma unroll 1
+        for (int kb = 0; kb < 2; ++kb) {
+          holes = both >> (2 * kb);
+          this->template block<CAREFUL>(s, 32 * kb, t * KT + 32 * kb);
+        }
+      }
+    };
+    if constexpr (!CAREFUL)
+      for (; t < out && now == 0; ++t) this->template pair<false>(begin(), 0, t * KT);
+    for (; t < off; ++t) masked();
+    for (; t < t1; ++t) begin();
+    __syncthreads();                     // the tiles are no longer read
+  }
+
+  __device__ __forceinline__ void run(const Sequence& s, const Place& p, int64_t x0, int64_t x1,
+                                      int64_t cost, int slot) {
+    const int in_tile = Tile::opaque(32 * static_cast<int>(threadIdx.x >> 6) + static_cast<int>(threadIdx.x & 31));
+    const int r = p.r * kMany + in_tile;
+    Tile::rows_of(s, p, r);
+    Tile::last_of(s, p.r, kMany);
+    const bool real = r < s.n * a.G;
+    hi = static_cast<int>(width);
+    hi_min = real ? hi : last;           // rows past the end ask for no mask
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2) {
+      hi = max(hi, __shfl_xor(hi, d));
+      hi_min = min(hi_min, __shfl_xor(hi_min, d));
+    }
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    hi_min = __builtin_amdgcn_readfirstlane(hi_min);
+    if constexpr (!CODED) {
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        const int row = lane / LPR, unit = (lane % LPR) ^ Tile::twist(i * RPI + row);
+        copy_at[i] = unit * 8 < a.D ? static_cast<uint32_t>(row * a.D * 2 + unit * 16) : 0x80000000u;
+      }
+    }
+    const int tiles = (last + KT - 1) / KT;
+    const int t0 = slot < 0 ? 0 : static_cast<int>(tiles * x0 / cost);
+    const int t1 = slot < 0 ? tiles : static_cast<int>(tiles * x1 / cost);
+    if (t0 < t1) {
+      pass<false>(t0, t1);
+      const bool again = Tile::not_finite();      // asked of all lanes
+      if (lane == 0) lds.odd[wave] = again;
+      __syncthreads();
+      bool any = false;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) any |= lds.odd[w] != 0;
+      if (__builtin_amdgcn_readfirstlane(any)) pass<true>(t0, t1);
+    } else {
+      Tile::zero();
+    }
+    l = half_sum(l);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) Tile::store(s, r, in_tile, slot, d, o[d]);
+    __syncthreads();                     // lds.odd is read
+  }
+};
+
+template <class T, int DP, int CAP, bool SLOPES, bool CODED>
+__global__ __launch_bounds__(64 * kWaves, 2) void paged_attention_kernel(const PagedArgs g) {
+  typedef FewRows<T, DP, CAP, SLOPES, CODED> Few;
+  typedef ManyRows<T, DP, CAP, SLOPES, CODED> Many;
+  static_assert(sizeof(typename Few::Tile::Lds) == sizeof(typename Many::Tile::Lds));
+  static_assert(sizeof(Few::Tile::Lds::k) + sizeof(Few::Tile::Lds::v) >=
+                    static_cast<size_t>(kWaves) * 32 * DP * 4,
+                "the waves' outputs are joined in the tiles' memory");
+  __shared__ alignas(16) uint8_t mem[sizeof(typename Few::Tile::Lds) + kWaves * 32 * 2 * 4];
+  const int64_t per_head = head_work(g), work = per_head * g.Hkv;
+  const int wgs = static_cast<int>(gridDim.x);
+  const int w = xcd_contiguous(static_cast<int>(blockIdx.x), wgs);
+  const int64_t each = share(g, work, wgs), c0 = w * each;
+  if (c0 >= work) return;
+  const int64_t c1 = min(c0 + each, work);
+  Place p = place(g, per_head, c0);
+  do {
+    if (p.start >= c1) break;
+    const Sequence s = sequence(g, p.b);
+    const int64_t cost = s.cost(p.r);
+    int64_t x0 = 0, x1 = cost;
+    int slot = -1;
+    if (left_whole(g, cost)) {
+      if (p.start < c0) {                // the workgroup before has it
+        if (!next_place(g, s, p)) break;
+        continue;
+      }
+    } else {
+      x0 = max(c0 - p.start, int64_t{0});
+      x1 = min(c1 - p.start, cost);
+      if (x0 > 0 || x1 < cost) slot = 2 * w + (x0 == 0 ? 1 : 0);
+    }
+    Scores scores;
+    const float ks = g.pages.k_scales != nullptr ? g.pages.k_scales[p.hk] : 1.f;
+    scores.scale2 = g.scale2 * ks;
+    scores.cap_in = fminf(g.cap_in * ks, 3.4028235e38f);
+    scores.cap2 = g.cap2;
+    if (s.few) {
+      Few t(g, scores, *reinterpret_cast<typename Few::Tile::Lds*>(mem));
+      t.run(s, p, x0, x1, cost, slot);
+    } else {
+      Many t(g, scores, *reinterpret_cast<typename Many::Tile::Lds*>(mem));
+      t.run(s, p, x0, x1, cost, slot);
+    }
+    if (!next_place(g, s, p)) break;
+  } while (true);
+}
+
+template <class T, int DP, int CAP, bool SLOPES>
+void launch_e(const PagedArgs& g, unsigned grid, hipStream_t stream) {
+  if (g.pages.coded)
+    hipLaunchKernelGGL((paged_attention_kernel<T, DP, CAP, SLOPES, true>), dim3(grid), dim3(64 * kWaves), 0,
+                       stream, g);
+  else
+    hipLaunchKernelGGL((paged_attention_kernel<T, DP, CAP, SLOPES, false>), dim3(grid), dim3(64 * kWaves), 0,
+                       stream, g);
+}
+template <class T, int DP, int CAP>
+void launch_s(const PagedArgs& g, unsigned grid, hipStream_t stream) {
+  g.slopes != nullptr ? launch_e<T, DP, CAP, true>(g, grid, stream) : launch_e<T, DP, CAP, false>(g, grid, stream);
+}
+
+}  // namespace
+
+template <class T, int DP>
+void launch_paged_tiles(const PagedArgs& g, unsigned grid, hipStream_t stream) {
+  g.cap == kNoCap     ? launch_s<T, DP, kNoCap>(g, grid, stream)
+  : g.cap == kNearCap ? launch_s<T, DP, kNearCap>(g, grid, stream)
+                      : launch_s<T, DP, kAnyCap>(g, grid, stream);
+}
+
+}  // namespace svdq

@@ -187,7 +187,13 @@ def test_hidden_keys_do_not_reach_an_output(sq, kind, n):
     got = run(sq, q, p, [0, n, 2 * n])
     keep = torch.ones(2 * n, dtype=torch.bool)
     keep[n - 1] = False
-    assert torch.equal(got[keep], clean[keep]) and bool(torch.isnan(got[n - 1]).all())
+    # Not bit for bit: the pass that is repeated for such values raises a row's reference at other
+    # keys, and an exponential's argument x - m, |x - m| < 2^7, is rounded to 2^-17 of a base-2 logit
+    # against each, which the bound's 4 * 2^-24 (2 + |top|) dx and the weights' half step both hold.
+    ref, bound, _ = P.attention(q, p, [0, n, 2 * n], [held, held], 64 ** -0.5)
+    R.assert_within(got, ref, bound)
+    R.assert_within(clean[keep], ref[keep], bound[keep])
+    assert bool(torch.isnan(got[n - 1]).all())
     if not coded:
         p = P.Pool([held], 2, 64, dtype, coded, 16).cuda()
         page, row = int(p.tables[0, (held - 1) // 16]), (held - 1) % 16
