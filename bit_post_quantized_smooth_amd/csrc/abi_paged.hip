@@ -182,7 +182,7 @@ int svdq_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, int
   g.Hq = static_cast<int>(Hq);
   g.Hkv = static_cast<int>(Hkv);
   g.D = static_cast<int>(D);
-  return check_hip(launch_heads(g, dtype, kNoPages, stream), fn);
+  return check_hip(launch_heads(g, dtype, stream), fn);
 }
 
 int svdq_paged_write(const void* Q, const void* K, const void* V, void* Q_out, int dtype, int64_t T,
@@ -234,7 +234,7 @@ int svdq_paged_write(const void* Q, const void* K, const void* V, void* Q_out, i
   g.Hq = static_cast<int>(Hq);
   g.Hkv = static_cast<int>(Hkv);
   g.D = static_cast<int>(D);
-  return check_hip(launch_heads(g, dtype, g.pages.coded ? kCodePages : kHalfPages, stream), fn);
+  return check_hip(launch_heads(g, dtype, stream), fn);
 }
 
 int svdq_paged_read(const void* k_pages, const void* v_pages, int cache_dtype, int64_t pages,
@@ -309,8 +309,7 @@ size_t svdq_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t capaci
                                             Hq, Hkv, D);
   clear_error();                       // a size query reports by its 0 alone
   if (s != SVDQ_OK) return 0;
-  const PartBytes p = paged_attention_parts(T, B, capacity, Hkv, Hq / Hkv, D);
-  return p.ml + p.o;
+  return paged_attention_parts(T, B, capacity, Hkv, Hq / Hkv, D).all();
 }
 
 int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t Hq, int64_t Hkv,
@@ -371,10 +370,12 @@ int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t
   g.D = static_cast<int>(D);
   g.capacity = static_cast<int>(capacity);
   const PartBytes parts = paged_attention_parts(T, B, capacity, Hkv, Hq / Hkv, D);
-  if (parts.o > 0 && ws != nullptr && ws_bytes >= parts.ml + parts.o) {
+  if (parts.o > 0 && ws != nullptr && ws_bytes >= parts.all()) {
+    uint8_t* base = static_cast<uint8_t*>(ws);
     g.part_rows = T * (Hq / Hkv) <= 32 ? 32 : 128;
-    g.part_ml = static_cast<float*>(ws);
-    g.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + parts.ml);
+    g.cuts = reinterpret_cast<Cut*>(base);
+    g.part_ml = reinterpret_cast<float*>(base + parts.cuts);
+    g.part_o = reinterpret_cast<float*>(base + parts.cuts + parts.ml);
   }
   return check_hip(launch_paged_attention(g, dtype, stream), fn);
 }

@@ -34,20 +34,19 @@ struct HeadsArgs {
   const double* freqs;             // radians per position of each pair
   const float* q_gain;
   const float* k_gain;
-  const int32_t* slots;            // per token, with pages
+  const int32_t* slots;            // per token; null: no pages
   Pages pages;
   float factor, eps;
   int pairs;                       // 0: no rotation
   int interleaved, norm;
   int T, Hq, Hkv, D;
-  int heads, chunks;               // set by launch_heads
+  int heads, q_chunks, k_chunks, chunks;   // set by launch_heads
+  float inv_D;
 };
-
-enum { kNoPages = 0, kHalfPages = 1, kCodePages = 2 };
 
 // Whether one launch covers T tokens of this many heads.
 bool heads_fit(int64_t T, int64_t heads);
-hipError_t launch_heads(HeadsArgs g, int dtype, int store, hipStream_t stream);
+hipError_t launch_heads(HeadsArgs g, int dtype, hipStream_t stream);
 
 struct ReadArgs {
   Pages pages;

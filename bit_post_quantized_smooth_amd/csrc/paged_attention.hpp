@@ -10,6 +10,15 @@
 
 namespace svdq {
 
+// The tile that a workgroup is the first to have a part of; parts 0: it has none. Its own
+// part is the second of its two, those of the workgroups behind it are their first.
+struct Cut {
+  int32_t parts, hk;
+  int32_t first;             // the sequence's first token
+  int32_t row, rows;         // the tile's first row and number of rows
+  int32_t pad[3];
+};
+
 // Strides in elements: _t token, _h head; channels are contiguous.
 struct PagedArgs {
   const void* q;
@@ -20,7 +29,8 @@ struct PagedArgs {
   const int32_t* lengths;    // B: tokens of each sequence in the cache
   const int32_t* starts;     // B + 1: each sequence's first token among the T
   const float* slopes;       // per query head, or null
-  float* part_ml;            // parts: maximum and sum per row
+  Cut* cuts;                 // per workgroup
+  float* part_ml;            // parts, two per workgroup: maximum and sum per row
   float* part_o;             // parts: unnormalized outputs, D per row
   // as in AttnArgs, without the head's scale
   int q_sign;
@@ -38,9 +48,10 @@ struct PagedArgs {
 constexpr int64_t kMostGroup = 256;
 constexpr int64_t kMostKeys = int64_t{1} << 26;
 
-// Bytes of the parts' maxima and sums, and of their outputs, on the current device.
+// Bytes of the cuts, the parts' maxima and sums, and their outputs, on the current device.
 struct PartBytes {
-  size_t ml, o;
+  size_t cuts, ml, o;
+  size_t all() const { return cuts + ml + o; }
 };
 PartBytes paged_attention_parts(int64_t T, int64_t B, int64_t capacity, int64_t Hkv, int64_t G,
                                 int64_t D);

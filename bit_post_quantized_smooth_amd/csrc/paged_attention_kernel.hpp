@@ -62,8 +62,8 @@ struct PageWindow {
     at = group & ~63;
     now = fetch(at);
     then = fetch(at + 64);
-    see();
   }
+  // Once they are needed: whoever begins may have other loads to send first.
   __device__ __forceinline__ void see() {
     there = __builtin_amdgcn_ballot_w64(now >= 0 && now < g->pages.count);
   }
@@ -102,7 +102,7 @@ struct PagedTile : AttentionCore<T, DP, RW, CAP, SLOPES, 128, Scores, true> {
 
   const PagedArgs& a;
   PageWindow pages;
-  int hk, b, last;                                  // last: keys that any row of the tile sees
+  int hk, last;                                     // last: keys that any row of the tile sees
   float vscale;
   // the lane's share of a fetch: its place in the rows (beyond any buffer past D) and in LDS
   uint32_t fetch_at;
@@ -173,8 +173,7 @@ struct PagedTile : AttentionCore<T, DP, RW, CAP, SLOPES, 128, Scores, true> {
     wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     rl = lane & 31;
     h = lane >> 5;
-    hk = p.hk;
-    b = p.b;
+    hk = uniform(p.hk);
     holes = 0;
     vscale = a.pages.v_scales != nullptr ? a.pages.v_scales[hk] : 1.f;
     fetch_at = 16 * (lane % LPR) < a.D * ESIZE
@@ -192,24 +191,27 @@ struct PagedTile : AttentionCore<T, DP, RW, CAP, SLOPES, 128, Scores, true> {
     const int hi = a.causal ? min(s.length, pos + 1) : s.length;
     lo = 0;
     width = real && hi > 0 ? static_cast<uint32_t>(hi) : 0u;
+    // Loads without a branch, from the first row and channels where there is nothing to
+    // load; queries() makes operands of them when the first keys are on their way.
     const T* qp = static_cast<const T*>(a.q) + (s.first + static_cast<int64_t>(i)) * a.q_t + head * a.q_h;
 #pragma unroll
     for (int t = 0; t < DS; ++t) {
       const int c = (2 * t + h) * 8;
-      v4i z = v4i{0, 0, 0, 0};
-      if (real && c < a.D && a.q_sign != 0) {
-        z = *reinterpret_cast<const v4i*>(qp + c);
-        if (a.q_sign < 0) z = z ^ static_cast<int>(0x80008000u);
-      }
+      qf[t] = __builtin_bit_cast(vec, *reinterpret_cast<const v4i*>(qp + (c < a.D ? c : 0)));
+    }
+  }
+  // Negated for a negative scale, 0 for a scale of 0 and where nothing was loaded.
+  __device__ __forceinline__ void queries(bool real) {
+    const int sign = a.q_sign < 0 ? static_cast<int>(0x80008000u) : 0;
+#pragma unroll
+    for (int t = 0; t < DS; ++t) {
+      const int c = (2 * t + h) * 8, keep = real && c < a.D && a.q_sign != 0 ? -1 : 0;
+      v4i z = __builtin_bit_cast(v4i, qf[t]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] = (z[e] ^ sign) & keep;
       qf[t] = __builtin_bit_cast(vec, z);
     }
   }
-  // The keys that any of the tile's rows sees.
-  __device__ __forceinline__ void last_of(const Sequence& s, int r, int rows) {
-    const int top = min(s.n, ((r + 1) * rows + a.G - 1) / a.G);     // queries before its end
-    last = a.causal ? max(0, min(s.length, s.length - s.n + top)) : s.length;
-  }
-
   __device__ __forceinline__ bool not_finite() const {
     bool odd = false;
 #pragma unroll
@@ -219,39 +221,28 @@ struct PagedTile : AttentionCore<T, DP, RW, CAP, SLOPES, 128, Scores, true> {
     return __builtin_amdgcn_ballot_w64(odd) != 0;
   }
 
-  // Output block d of row r: the outputs, or the part `slot`.
-  __device__ __forceinline__ void store(const Sequence& s, int r, int in_tile, int slot, int d, const v16f& od) {
-    if (r >= s.n * a.G) return;
+  // Channels ch .. ch + 3 of row r (row in_tile of the tile), whose weights sum to l, under
+  // the reference m: the outputs, or in the part `slot`.
+  __device__ __forceinline__ void store(const Sequence& s, int r, int in_tile, int slot, int ch, v4f x) {
+    if (ch >= a.D) return;
     if (slot >= 0) {
       const int64_t row = static_cast<int64_t>(slot) * a.part_rows + in_tile;
-      if (h == 0 && d == 0) {
+      if (ch == 0) {
         a.part_ml[2 * row] = m;
         a.part_ml[2 * row + 1] = l;
       }
-      if (l == 0.f) return;              // the join reads no outputs of such a row
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int ch = 32 * d + 8 * e + 4 * h;
-        if (ch < a.D)
-          *reinterpret_cast<v4f*>(a.part_o + row * a.D + ch) =
-              v4f{od[4 * e], od[4 * e + 1], od[4 * e + 2], od[4 * e + 3]};
-      }
+      // the join reads no outputs of a row without weights
+      if (l != 0.f) *reinterpret_cast<v4f*>(a.part_o + row * a.D + ch) = x;
       return;
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     T* op = static_cast<T*>(a.out) + (s.first + static_cast<int64_t>(r / a.G)) * a.o_t +
             (hk * a.G + r % a.G) * a.o_h;
+    typedef T vec4 __attribute__((ext_vector_type(4)));
+    vec4 y;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int ch = 32 * d + 8 * e + 4 * h;
-      if (ch < a.D) {
-        typedef T vec4 __attribute__((ext_vector_type(4)));
-        vec4 y;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = static_cast<T>(od[4 * e + c] * inv * vscale);
-        *reinterpret_cast<vec4*>(op + ch) = y;
-      }
-    }
+    for (int c = 0; c < 4; ++c) y[c] = static_cast<T>(x[c] * inv * vscale);
+    *reinterpret_cast<vec4*>(op + ch) = y;
   }
 };
 
@@ -296,14 +287,17 @@ struct FewRows : PagedTile<T, DP, 1, CAP, SLOPES, CODED> {
     holes = x.gone;
   }
 
+  // Blocks block0 + wave, + 4, ... before block1, whose page numbers are on their way.
   template <bool CAREFUL>
-  __device__ __forceinline__ void pass(int block0, int block1) {
-    Tile::zero();
+  __device__ __forceinline__ void pass(int block0, int block1, bool real) {
     int i = block0 + wave;
-    if (i >= block1) return;
-    pages.begin(a, Tile::b, 2 * i);
     Ahead x;
-    get(x, i);
+    if (i < block1) {
+      pages.see();
+      get(x, i);
+    }
+    if constexpr (!CAREFUL) Tile::queries(real);
+    Tile::zero();
     for (; i < block1; i += kWaves) {
       set(x);
       if (i + kWaves < block1) get(x, i + kWaves);
@@ -313,56 +307,69 @@ struct FewRows : PagedTile<T, DP, 1, CAP, SLOPES, CODED> {
 
   __device__ __forceinline__ void run(const Sequence& s, const Place& p, int64_t x0, int64_t x1,
                                       int64_t cost, int slot) {
-    Tile::rows_of(s, p, Tile::opaque(threadIdx.x & 31));
-    Tile::last_of(s, p.r, kFew);
+    wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    last = uniform(s.length);            // the last query sees them all
     const int blocks = (last + 31) / 32;
-    const int b0 = slot < 0 ? 0 : static_cast<int>(blocks * x0 / cost);
-    const int b1 = slot < 0 ? blocks : static_cast<int>(blocks * x1 / cost);
-    pass<false>(b0, b1);
-    if (Tile::not_finite()) pass<true>(b0, b1);
+    const int b0 = uniform(x0 > 0 ? steps_before(a, blocks, x0, cost) : 0);
+    const int b1 = uniform(x1 < cost ? steps_before(a, blocks, x1, cost) : blocks);
+    pages.begin(a, p.b, 2 * (b0 + wave));
+    const int rows = s.n * a.G;
+    Tile::rows_of(s, p, Tile::opaque(threadIdx.x & 31));
+    pass<false>(b0, b1, rl < rows);
+    if (Tile::not_finite()) {
+      pages.begin(a, p.b, 2 * (b0 + wave));
+      pass<true>(b0, b1, rl < rows);
+    }
     l = half_sum(l);
-    join(s, slot);
+    join(s, slot, rows);
   }
 
-  // Adds the waves' outputs in wave order, scaled to the common maximum: output block d
-  // by wave d.
-  __device__ __forceinline__ void join(const Sequence& s, int slot) {
+  // Adds the waves' outputs in wave order, scaled to the common maximum: the rows that
+  // there are, 32 lanes a row, 4 channels each.
+  static constexpr int STRIDE = DP + 4;             // floats; rows on different banks
+  static constexpr size_t JOIN_BYTES = (kWaves * 32 * STRIDE + kWaves * 32 * 2) * 4;
+
+  __device__ __forceinline__ void join(const Sequence& s, int slot, int rows) {
     float* mem = reinterpret_cast<float*>(&lds);
-    float* ml = reinterpret_cast<float*>(&lds + 1);
+    float* ml = mem + kWaves * 32 * STRIDE;
     __syncthreads();                     // the tiles are no longer read
-    if (h == 0) {
-      ml[(wave * 32 + rl) * 2] = m;
-      ml[(wave * 32 + rl) * 2 + 1] = l;
+    if (rl < rows) {
+      if (h == 0) {
+        ml[(wave * 32 + rl) * 2] = m;
+        ml[(wave * 32 + rl) * 2 + 1] = l;
+      }
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<v4f*>(mem + (wave * 32 + rl) * STRIDE + 32 * d + 8 * e + 4 * h) =
+              v4f{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
     }
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) mem[((wave * DB + d) * 16 + e) * 64 + lane] = o[d][e];
     __syncthreads();
-    if (wave < DB) {
-      float top = kNegInf;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml[(w * 32 + rl) * 2]);
-      // two above the largest: the sum of four finite partial outputs is finite
-      const float base = top == kNegInf ? 0.f : top + 2.f;
-      float f[kWaves];
-      l = 0.f;
+    const int ch = 4 * (lane & 31);
+    for (int r = 2 * wave + h; r < rows; r += 2 * kWaves) {
+      float f[kWaves], top = kNegInf;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        f[w] = __builtin_amdgcn_exp2f(ml[(w * 32 + rl) * 2] - base);
-        l = __builtin_fmaf(ml[(w * 32 + rl) * 2 + 1], f[w], l);
+        f[w] = ml[(w * 32 + r) * 2];
+        top = fmaxf(top, f[w]);
       }
+      // two above the largest: the sum of four finite partial outputs is finite
+      const float base = top == kNegInf ? 0.f : top + 2.f;
       m = top == kNegInf ? top : base;
-      v16f sum;
+      l = 0.f;
+      v4f sum = v4f{0.f, 0.f, 0.f, 0.f};
+      if (ch < DP) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float v = 0.f;
+        for (int w = 0; w < kWaves; ++w) {
+          f[w] = __builtin_amdgcn_exp2f(f[w] - base);
+          l = __builtin_fmaf(ml[(w * 32 + r) * 2 + 1], f[w], l);
+          const v4f x = *reinterpret_cast<const v4f*>(mem + (w * 32 + r) * STRIDE + ch);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-          v = __builtin_fmaf(mem[((w * DB + wave) * 16 + e) * 64 + lane], f[w], v);
-        sum[e] = v;
+          for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(x[e], f[w], sum[e]);
+        }
+        Tile::store(s, r, r, slot, ch, sum);
       }
-      Tile::store(s, rl, rl, slot, wave, sum);
     }
     __syncthreads();                     // the next tile's rows may come
   }
@@ -415,11 +422,12 @@ struct ManyRows : PagedTile<T, DP, 4, CAP, SLOPES, CODED> {
   }
 
   template <bool CAREFUL>
-  __device__ __forceinline__ void pass(int t0, int t1) {
-    Tile::zero();
-    pages.begin(a, Tile::b, t0 * (KT / kGroupKeys));
+  __device__ __forceinline__ void pass(int t0, int t1, bool real) {
+    pages.see();
     get(t0, 0);
     uint32_t now = gone;
+    if constexpr (!CAREFUL) Tile::queries(real);
+    Tile::zero();
     if constexpr (CODED) {
       set(0);
       if (t0 + 1 < t1) get(t0 + 1, 1);
@@ -472,10 +480,15 @@ struct ManyRows : PagedTile<T, DP, 4, CAP, SLOPES, CODED> {
 
   __device__ __forceinline__ void run(const Sequence& s, const Place& p, int64_t x0, int64_t x1,
                                       int64_t cost, int slot) {
+    const int top = min(s.n, ((p.r + 1) * kMany + a.G - 1) / a.G);  // queries before the tile's end
+    last = uniform(a.causal ? max(0, min(s.length, s.length - s.n + top)) : s.length);
+    const int tiles = (last + KT - 1) / KT;
+    const int t0 = uniform(x0 > 0 ? steps_before(a, tiles, x0, cost) : 0);
+    const int t1 = uniform(x1 < cost ? steps_before(a, tiles, x1, cost) : tiles);
+    pages.begin(a, p.b, t0 * (KT / kGroupKeys));
     const int in_tile = Tile::opaque(32 * static_cast<int>(threadIdx.x >> 6) + static_cast<int>(threadIdx.x & 31));
     const int r = p.r * kMany + in_tile;
     Tile::rows_of(s, p, r);
-    Tile::last_of(s, p.r, kMany);
     const bool real = r < s.n * a.G;
     hi = static_cast<int>(width);
     hi_min = real ? hi : last;           // rows past the end ask for no mask
@@ -493,24 +506,29 @@ struct ManyRows : PagedTile<T, DP, 4, CAP, SLOPES, CODED> {
         copy_at[i] = unit * 8 < a.D ? static_cast<uint32_t>(row * a.D * 2 + unit * 16) : 0x80000000u;
       }
     }
-    const int tiles = (last + KT - 1) / KT;
-    const int t0 = slot < 0 ? 0 : static_cast<int>(tiles * x0 / cost);
-    const int t1 = slot < 0 ? tiles : static_cast<int>(tiles * x1 / cost);
     if (t0 < t1) {
-      pass<false>(t0, t1);
+      pass<false>(t0, t1, real);
       const bool again = Tile::not_finite();      // asked of all lanes
       if (lane == 0) lds.odd[wave] = again;
       __syncthreads();
       bool any = false;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) any |= lds.odd[w] != 0;
-      if (__builtin_amdgcn_readfirstlane(any)) pass<true>(t0, t1);
+      if (__builtin_amdgcn_readfirstlane(any)) {
+        pages.begin(a, p.b, t0 * (KT / kGroupKeys));
+        pass<true>(t0, t1, real);
+      }
     } else {
       Tile::zero();
     }
     l = half_sum(l);
+    if (real)
 #pragma unroll
-    for (int d = 0; d < DB; ++d) Tile::store(s, r, in_tile, slot, d, o[d]);
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          Tile::store(s, r, in_tile, slot, 32 * d + 8 * e + 4 * h,
+                      v4f{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]});
     __syncthreads();                     // lds.odd is read
   }
 };
@@ -520,32 +538,39 @@ __global__ __launch_bounds__(64 * kWaves, 2) void paged_attention_kernel(const P
   typedef FewRows<T, DP, CAP, SLOPES, CODED> Few;
   typedef ManyRows<T, DP, CAP, SLOPES, CODED> Many;
   static_assert(sizeof(typename Few::Tile::Lds) == sizeof(typename Many::Tile::Lds));
-  static_assert(sizeof(Few::Tile::Lds::k) + sizeof(Few::Tile::Lds::v) >=
-                    static_cast<size_t>(kWaves) * 32 * DP * 4,
-                "the waves' outputs are joined in the tiles' memory");
-  __shared__ alignas(16) uint8_t mem[sizeof(typename Few::Tile::Lds) + kWaves * 32 * 2 * 4];
-  const int64_t per_head = head_work(g), work = per_head * g.Hkv;
+  constexpr size_t kTiles = sizeof(typename Few::Tile::Lds);
+  __shared__ alignas(16) uint8_t mem[kTiles > Few::JOIN_BYTES ? kTiles : Few::JOIN_BYTES];
+  fetch_arguments(g);
+  Line line(g);
+  const int64_t work = line.per_head * g.Hkv;
   const int wgs = static_cast<int>(gridDim.x);
   const int w = xcd_contiguous(static_cast<int>(blockIdx.x), wgs);
-  const int64_t each = share(g, work, wgs), c0 = w * each;
+  const int64_t each = share(g, work, wgs), c0 = w * each, c1 = min(c0 + each, work);
+  if (g.part_rows > 0 && threadIdx.x == 0) g.cuts[w].parts = 0;
   if (c0 >= work) return;
-  const int64_t c1 = min(c0 + each, work);
-  Place p = place(g, per_head, c0);
-  do {
-    if (p.start >= c1) break;
-    const Sequence s = sequence(g, p.b);
+  Sequence s;
+  Place p = place(g, line, c0, s);
+  for (bool more = true; more && p.start < c1; more = next_place(g, line, p, s)) {
     const int64_t cost = s.cost(p.r);
     int64_t x0 = 0, x1 = cost;
     int slot = -1;
-    if (left_whole(g, cost)) {
-      if (p.start < c0) {                // the workgroup before has it
-        if (!next_place(g, s, p)) break;
-        continue;
-      }
+    if (left_whole(g, s, cost)) {
+      if (p.start < c0) continue;        // the workgroup before has it
     } else {
-      x0 = max(c0 - p.start, int64_t{0});
-      x1 = min(c1 - p.start, cost);
+      x0 = cut_at(g, c0 - p.start);
+      x1 = cut_at(g, min(c1 - p.start, cost));
+      if (x1 == 0) continue;             // the workgroup behind has it all
       if (x0 > 0 || x1 < cost) slot = 2 * w + (x0 == 0 ? 1 : 0);
+      if (x0 == 0 && x1 < cost && threadIdx.x == 0) {
+        const int rows = s.few ? kFew : kMany;
+        Cut& cut = g.cuts[w];
+        int64_t left;
+        cut.parts = quotient(p.start + cost - 1, each, left) - w + 1;
+        cut.first = s.first;
+        cut.row = p.r * rows;
+        cut.rows = min(rows, s.n * g.G - p.r * rows);
+        cut.hk = p.hk;
+      }
     }
     Scores scores;
     const float ks = g.pages.k_scales != nullptr ? g.pages.k_scales[p.hk] : 1.f;
@@ -559,8 +584,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void paged_attention_kernel(const P
       Many t(g, scores, *reinterpret_cast<typename Many::Tile::Lds*>(mem));
       t.run(s, p, x0, x1, cost, slot);
     }
-    if (!next_place(g, s, p)) break;
-  } while (true);
+  }
 }
 
 template <class T, int DP, int CAP, bool SLOPES>

@@ -14,17 +14,39 @@ namespace {
 constexpr int kFew = 32, kMany = 128;     // rows of a tile
 constexpr int kGroupKeys = 16;            // keys that lie in one page together
 
-// Work is counted in keys of a tile of few rows, times G. A tile of many takes twice as
-// long per key; its start and end as long as kStart keys.
-constexpr int kStart = 128;
-constexpr int kWhole = 512;               // tiles up to this are not split
-constexpr int kLeast = 256;               // the smallest share of a workgroup
+// Work is counted in keys of a tile of few rows, times G. A tile of many rows takes twice
+// as long per key (per workgroup, two on a compute unit: 64 keys 2.4 us, where few rows take
+// 128 in 2.2). A tile's start and end take 8 us, as long as 448 keys (measured, one token for
+// each of 8 sequences of up to 8191, 32/8 heads: 36 us counting 128 of them, 33 with 384, 31
+// with 448 to 640). Tiles up to kWhole are not cut (8 prompts of 300 at the end of 900: 67 us;
+// 1024: 80), and a share is not below kLeast (3 sequences of 1000: 13.7 us, with 256 15.5;
+// one of 8191: 21.9 and 20.9).
+constexpr int kStart = 448;
+constexpr int kWholeFew = 960, kWholeMany = 768;
+constexpr int kLeast = 192;
+
+// The arguments, which lie in memory as far away as the host's, in one round of loads
+// instead of one where each is first needed.
+__device__ __forceinline__ void fetch_arguments(const PagedArgs& g) {
+  asm volatile("" ::"s"(g.q), "s"(g.o_t), "s"(g.pages.k_stride), "s"(g.pages.v_scales), "s"(g.tables),
+               "s"(g.part_ml), "s"(g.scale2), "s"(g.B), "s"(g.part_rows));
+}
 
 struct Sequence {
   int first, n, length;                   // tokens among the T; tokens in the cache
   bool few;
   int tiles;                              // of one key head
   int64_t fixed, step;                    // tile r: fixed + step * (r + 1)
+
+  __device__ __forceinline__ void set(const PagedArgs& g) {
+    const int rows = n * g.G;
+    few = rows <= kFew;
+    tiles = few ? (rows > 0 ? 1 : 0) : (rows + kMany - 1) / kMany;
+    const bool steps = g.causal && !few;
+    const int64_t keys = steps ? max(length - n, 0) : length;
+    fixed = static_cast<int64_t>(g.G) * (kStart + (few ? 1 : 2) * keys);
+    step = steps ? 2 * kMany : 0;
+  }
 
   __device__ __forceinline__ int64_t cost(int r) const { return fixed + step * (r + 1); }
   __device__ __forceinline__ int64_t before(int r) const {
@@ -37,22 +59,10 @@ __device__ __forceinline__ Sequence sequence(const PagedArgs& g, int b) {
   s.first = min(max(g.starts[b], 0), g.T);
   s.n = min(max(g.starts[b + 1], s.first), g.T) - s.first;
   s.length = g.pages.count > 0 ? min(max(g.lengths[b], 0), g.capacity) : 0;
-  const int rows = s.n * g.G;
-  s.few = rows <= kFew;
-  s.tiles = s.few ? (rows > 0 ? 1 : 0) : (rows + kMany - 1) / kMany;
-  const bool steps = g.causal && !s.few;
-  const int64_t keys = steps ? max(s.length - s.n, 0) : s.length;
-  s.fixed = static_cast<int64_t>(g.G) * (kStart + (s.few ? 1 : 2) * keys);
-  s.step = steps ? 2 * kMany : 0;
+  s.set(g);
   return s;
 }
 
-// Sequences 64 at a time, one a lane.
-__device__ __forceinline__ int64_t own_work(const PagedArgs& g, int b) {
-  if (b >= g.B) return 0;
-  const Sequence s = sequence(g, b);
-  return s.before(s.tiles);
-}
 __device__ __forceinline__ int64_t running_sum(int64_t x) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -62,77 +72,138 @@ __device__ __forceinline__ int64_t running_sum(int64_t x) {
   }
   return x;
 }
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-  const int lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
-  const int hi = __builtin_amdgcn_readfirstlane(static_cast<int>(x >> 32));
+__device__ __forceinline__ int64_t of_lane(int64_t x, int lane) {
+  const int lo = __builtin_amdgcn_readlane(static_cast<int>(x), lane);
+  const int hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), lane);
   return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 |
                               static_cast<uint32_t>(lo));
 }
 
-// The work of one key head.
-__device__ __forceinline__ int64_t head_work(const PagedArgs& g) {
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < g.B; b0 += 64)
-    sum += uniform(__shfl(running_sum(own_work(g, b0 + (threadIdx.x & 63))), 63));
-  return sum;
+// The wave's one value of x, in scalar registers: what comes out of vector arithmetic stays
+// in vector registers otherwise, and every load by an address made of it becomes a loop.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const int lo = uniform(static_cast<int>(x)), hi = uniform(static_cast<int>(x >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 |
+                              static_cast<uint32_t>(lo));
 }
+
+// a / b and what is left, for quotients below 2^24 (one multiplication by a reciprocal that
+// is good to that, put right by one; a division of 64 bits takes 130 instructions).
+__device__ __forceinline__ int quotient(int64_t a, int64_t b, int64_t& left) {
+  int q = uniform(static_cast<int>(static_cast<double>(a) * __builtin_amdgcn_rcp(static_cast<double>(b))));
+  left = a - q * b;
+  if (left < 0) {
+    left += b;
+    --q;
+  } else if (left >= b) {
+    left -= b;
+    ++q;
+  }
+  return q;
+}
+
+// The sequences 64 at a time, one a lane, with the work up to each one's end. Up to 64
+// are looked at once.
+struct Line {
+  Sequence own;
+  int64_t upto;
+  int at;                                 // the first of those held
+  int64_t per_head;                       // work of one key head
+
+  __device__ __forceinline__ void hold(const PagedArgs& g, int first) {
+    at = first;
+    const int b = first + static_cast<int>(threadIdx.x & 63);
+    own = sequence(g, b < g.B ? b : g.B - 1);
+    if (b >= g.B) own.tiles = 0;
+    upto = running_sum(own.before(own.tiles));
+  }
+  __device__ __forceinline__ Line(const PagedArgs& g) {
+    per_head = 0;
+    for (int b0 = 0; b0 < g.B; b0 += 64) {
+      hold(g, b0);
+      per_head += of_lane(upto, 63);
+    }
+  }
+  // Sequence b, the same for the whole wave.
+  __device__ __forceinline__ Sequence get(const PagedArgs& g, int b) {
+    if (b < at || b >= at + 64) hold(g, b & ~63);
+    const int lane = b - at;
+    Sequence s;
+    s.first = __builtin_amdgcn_readlane(own.first, lane);
+    s.n = __builtin_amdgcn_readlane(own.n, lane);
+    s.length = __builtin_amdgcn_readlane(own.length, lane);
+    s.set(g);
+    return s;
+  }
+};
 
 // A workgroup's place on the line: the tile that position c falls into.
 struct Place {
   int hk, b, r;
   int64_t start;                          // the tile's
 };
-__device__ __forceinline__ Place place(const PagedArgs& g, int64_t per_head, int64_t c) {
+__device__ __forceinline__ Place place(const PagedArgs& g, Line& line, int64_t c, Sequence& s) {
   Place p;
-  p.hk = static_cast<int>(c / per_head);
-  int64_t left = c - p.hk * per_head;
+  int64_t left;
+  p.hk = quotient(c, line.per_head, left);
   p.b = 0;
-  p.r = 0;
   for (int b0 = 0; b0 < g.B; b0 += 64) {
-    const int64_t upto = running_sum(own_work(g, b0 + (threadIdx.x & 63)));
-    const uint64_t behind = __builtin_amdgcn_ballot_w64(upto > left);
+    if (line.at != b0) line.hold(g, b0);
+    const uint64_t behind = __builtin_amdgcn_ballot_w64(line.upto > left);
     if (behind != 0) {
       const int at = __builtin_ctzll(behind);
-      if (at > 0) left -= uniform(__shfl(upto, at - 1));
+      if (at > 0) left -= of_lane(line.upto, at - 1);
       p.b = b0 + at;
       break;
     }
-    left -= uniform(__shfl(upto, 63));
+    left -= of_lane(line.upto, 63);
   }
-  const Sequence s = sequence(g, p.b);
+  s = line.get(g, p.b);
   int lo = 0, hi = s.tiles - 1;           // the last tile that starts at or before left
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
     if (s.before(mid) <= left) lo = mid;
     else hi = mid - 1;
   }
-  p.b = __builtin_amdgcn_readfirstlane(p.b);
-  p.r = __builtin_amdgcn_readfirstlane(lo);
-  p.start = uniform(c - (left - s.before(lo)));
+  p.r = lo;
+  p.start = c - (left - s.before(lo));
   return p;
 }
-// The next tile, if there is one.
-__device__ __forceinline__ bool next_place(const PagedArgs& g, const Sequence& s, Place& p) {
+// The next tile and its sequence, if there is one.
+__device__ __forceinline__ bool next_place(const PagedArgs& g, Line& line, Place& p, Sequence& s) {
   p.start += s.cost(p.r);
   if (++p.r < s.tiles) return true;
   p.r = 0;
-  int heads = 2;                          // none holds tokens: one round is enough
-  while (heads > 0) {
+  while (true) {
     if (++p.b == g.B) {
       p.b = 0;
-      --heads;
       if (++p.hk == g.Hkv) return false;
     }
-    if (sequence(g, p.b).tiles > 0) return true;
+    s = line.get(g, p.b);
+    if (s.tiles > 0) return true;         // some are, or there was no place
   }
-  return false;
 }
 
+// What a workgroup takes of the line: no less than work / wgs.
 __device__ __forceinline__ int64_t share(const PagedArgs& g, int64_t work, int wgs) {
-  return max((work + wgs - 1) / wgs, static_cast<int64_t>(kLeast) * g.G);
+  const double part = static_cast<double>(work) * __builtin_amdgcn_rcp(static_cast<double>(wgs));
+  const int64_t each = uniform(static_cast<int64_t>(part * (1.0 + 0x1p-20))) + 1;
+  return max(each, static_cast<int64_t>(kLeast) * g.G);
 }
-__device__ __forceinline__ bool left_whole(const PagedArgs& g, int64_t cost) {
-  return g.part_rows == 0 || cost <= static_cast<int64_t>(kWhole) * g.G;
+// A place x on a tile's stretch of work at which it may be cut: a tile's start is not divided.
+__device__ __forceinline__ int64_t cut_at(const PagedArgs& g, int64_t x) {
+  return x <= static_cast<int64_t>(kStart) * g.G ? 0 : x;
+}
+// The steps of a tile that lie before place x, 0 < x < cost: the same for the workgroups on
+// both sides of it.
+__device__ __forceinline__ int steps_before(const PagedArgs& g, int steps, int64_t x, int64_t cost) {
+  const int64_t start = static_cast<int64_t>(kStart) * g.G;
+  const double part = static_cast<double>(x - start) * __builtin_amdgcn_rcp(static_cast<double>(cost - start));
+  return min(steps, uniform(static_cast<int>(static_cast<double>(steps) * part)));
+}
+__device__ __forceinline__ bool left_whole(const PagedArgs& g, const Sequence& s, int64_t cost) {
+  return g.part_rows == 0 || cost <= static_cast<int64_t>(s.few ? kWholeFew : kWholeMany) * g.G;
 }
 
 }  // namespace

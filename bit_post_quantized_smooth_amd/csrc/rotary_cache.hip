@@ -37,17 +37,39 @@ struct Vec8 {
   typedef T vec __attribute__((ext_vector_type(8)));
 };
 
-// Where a channel's partner lies: the next or last channel, 8 channels of another
-// lane, or (pairs not a multiple of 8) anywhere, read from memory again.
-enum { kStay = 0, kNext = 1, kLanes = 2, kFar = 3 };
+// Where a channel's partner lies: there is none; the next or last channel; in the lane
+// half a head away, where all LPR lanes' channels turn; in another lane; or (pairs not a
+// multiple of 8) anywhere, read from memory again.
+enum { kStay, kNext, kOpposite, kLanes, kFar };
+
+template <int CTRL, int BANKS>
+__device__ __forceinline__ float dpp(float old, float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, x), CTRL,
+                                         0xF, BANKS, false));
+}
+// The value of the lane half of LPR lanes away, within 16 lanes' registers.
+template <int LPR>
+__device__ __forceinline__ float opposite(float x) {
+  if constexpr (LPR == 16) return dpp<0x128, 0xF>(x, x);             // rotate by 8
+  return dpp<0x114, 0xA>(dpp<0x104, 0x5>(x, x), x);                  // 4 up, 4 down
+}
+// The sum over LPR lanes: neighbours, pairs, mirrored fours, mirrored eights.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+  x += dpp<0xB1, 0xF>(x, x);
+  x += dpp<0x4E, 0xF>(x, x);
+  x += dpp<0x141, 0xF>(x, x);
+  if constexpr (LPR == 16) x += dpp<0x140, 0xF>(x, x);
+  return x;
+}
 
 // e4m3 codes of 8 values, two dwords
 __device__ __forceinline__ int2 codes8(const float (&u)[VEC], float inv) {
   float x[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    const float y = u[e] * inv;
-    const float kept = fminf(fmaxf(y, -448.f), 448.f);
+    const float kept = __builtin_amdgcn_fmed3f(u[e] * inv, -448.f, 448.f);
     x[e] = fabsf(u[e]) < __builtin_inff() ? kept : __builtin_nanf("");
   }
   int lo = 0, hi = 0;
@@ -66,172 +88,176 @@ __device__ __forceinline__ void store16(T* p, const float (&u)[VEC]) {
   *reinterpret_cast<typename Vec8<T>::vec*>(p) = y;
 }
 
-// LPR lanes per head, HPG heads of a token per group of lanes.
-template <class T, int STORE, int LPR, int HPG>
+// LPR lanes per head; a workgroup takes up to HPG heads of one operand for 256 / LPR tokens,
+// so that which operand it is, and whether it turns, is the same for all its lanes. Loads
+// have no branch around them: what lies behind the last token, head or channel reads the
+// last one again and is not stored.
+template <class T, int MODE, int LPR, int HPG>
 __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs g) {
   typedef typename Vec8<T>::vec vec;
-  const int64_t group = static_cast<int64_t>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
-  const int t = static_cast<int>(group / g.chunks);
-  if (t >= g.T) return;                            // all lanes of a group together
-  const int head0 = static_cast<int>(group % g.chunks) * HPG;
-  const int rl = threadIdx.x % LPR, c0 = VEC * rl;
-  const bool active = c0 < g.D;
-  const int64_t slot = STORE != kNoPages ? g.slots[t] : -1;
-  const bool stored = STORE == kNoPages ||
-                      (slot >= 0 && slot < (g.pages.count << g.pages.page_log2));
+  const int chunk = static_cast<int>(blockIdx.x) % g.chunks;
+  const int tokens = static_cast<int>(blockIdx.x) / g.chunks;
+  const bool is_q = chunk < g.q_chunks, is_v = chunk >= g.q_chunks + g.k_chunks;
+  const int head0 = HPG * (is_q ? chunk : is_v ? chunk - g.q_chunks - g.k_chunks : chunk - g.q_chunks);
+  const int H = is_q ? g.Hq : g.Hkv;
+  const T* src = static_cast<const T*>(is_q ? g.q : is_v ? g.v : g.k);
+  const int64_t src_t = is_q ? g.q_t : is_v ? g.v_t : g.k_t;
+  const int64_t src_h = is_q ? g.q_h : is_v ? g.v_h : g.k_h;
+  const bool turn = MODE != kStay && !is_v, norm = g.norm && !is_v;
 
-  // source of head h of the list queries, keys, values
-  auto source = [&](int h) {
-    const bool is_q = h < g.Hq, is_k = h < g.Hq + g.Hkv;
-    const T* base = static_cast<const T*>(is_q ? g.q : is_k ? g.k : g.v);
-    const int64_t st = is_q ? g.q_t : is_k ? g.k_t : g.v_t, sh = is_q ? g.q_h : is_k ? g.k_h : g.v_h;
-    const int hh = is_q ? h : is_k ? h - g.Hq : h - g.Hq - g.Hkv;
-    return base + t * st + hh * sh;
-  };
+  const int rl = threadIdx.x % LPR, c0 = VEC * rl;
+  const int64_t t0 = static_cast<int64_t>(tokens) * (kThreads / LPR) + threadIdx.x / LPR;
+  const int64_t t = t0 < g.T ? t0 : g.T - 1;
+  const bool inside = c0 < g.D;
+  const int c = inside ? c0 : 0;
+
+  src += t * src_t + c;
   vec raw[HPG];
 #pragma unroll
   for (int i = 0; i < HPG; ++i) {
-    const int h = head0 + i;
+    const int h = head0 + i < H ? head0 + i : H - 1;
+    raw[i] = *reinterpret_cast<const vec*>(src + h * src_h);
+  }
+  const int64_t slot = g.slots != nullptr && !is_q ? g.slots[t] : 0;
+  const float* gain = is_q ? g.q_gain : g.k_gain;
+  float gains[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) raw[i][e] = static_cast<T>(0.f);
-    if (active && h < g.heads && (h < g.Hq || stored))
-      raw[i] = *reinterpret_cast<const vec*>(source(h) + c0);
+  for (int e = 0; e < VEC; ++e) gains[e] = 1.f;
+  if (norm && gain != nullptr) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) gains[e] = gain[c + e];
+  }
+  // cosine and signed sine of each channel; the channels behind R stay as they are
+  const int R = 2 * g.pairs;
+  float cs[VEC], sn[VEC];
+  if (turn) {
+    const int32_t position = g.positions[t];
+    double freq[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (MODE == kNext && (e & 1)) continue;
+      const int ch = c0 + e;
+      const int pair = ch >= R ? 0 : MODE == kNext ? ch / 2 : ch < g.pairs ? ch : ch - g.pairs;
+      freq[e] = g.freqs[pair];
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const bool first = MODE == kNext ? (e & 1) == 0 : c0 + e < g.pairs;
+      if (MODE == kNext && (e & 1)) {
+        cs[e] = cs[e - 1];
+        sn[e] = -sn[e - 1];
+        continue;
+      }
+      cos_sin(position, freq[e], cs[e], sn[e]);
+      cs[e] = cs[e] * g.factor;
+      sn[e] = sn[e] * (first ? -g.factor : g.factor);
+    }
   }
 
-  const int R = 2 * g.pairs;
-  const int mode = R == 0 ? kStay : g.interleaved ? kNext : g.pairs % VEC == 0 ? kLanes : kFar;
-  // cosine and signed sine of each channel; the channels behind R stay as they are
-  float cs[VEC], sn[VEC];
-  int other[VEC];                                  // the partner's channel
-  if (mode != kStay) {
-    const int32_t position = g.positions[t];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = c0 + e;
-      const bool first = mode == kNext ? (e & 1) == 0 : c < g.pairs;
-      const int pair = mode == kNext ? c / 2 : first ? c : c - g.pairs;
-      other[e] = mode == kNext ? c ^ 1 : first ? c + g.pairs : c - g.pairs;
-      cs[e] = 1.f;
-      sn[e] = 0.f;
-      if (c < R) {
-        if (mode == kNext && !first) {
-          cs[e] = cs[e - (e & 1)];
-          sn[e] = -sn[e - (e & 1)];
-        } else {
-          cos_sin(position, g.freqs[pair], cs[e], sn[e]);
-          cs[e] = cs[e] * g.factor;
-          sn[e] = sn[e] * (first ? -g.factor : g.factor);
-        }
-      }
-    }
+  // where the rows go
+  const Pages& pg = g.pages;
+  const bool paged = g.slots != nullptr && !is_q;
+  const bool stored = inside && t0 < g.T && (!paged || (slot >= 0 && slot < (pg.count << pg.page_log2)));
+  char* to;
+  int64_t to_h;
+  if (paged) {
+    const int esize = pg.coded ? 1 : 2;
+    to = static_cast<char*>(is_v ? pg.v : pg.k) + (slot >> pg.page_log2) * (is_v ? pg.v_stride : pg.k_stride) +
+         ((slot & ((1 << pg.page_log2) - 1)) * g.D + c) * esize;
+    to_h = static_cast<int64_t>(g.D * esize) << pg.page_log2;
+  } else {
+    to = static_cast<char*>(is_q ? g.q_out : g.k_out) + (t * (is_q ? g.qo_t : g.ko_t) + c) * 2;
+    to_h = (is_q ? g.qo_h : g.ko_h) * 2;
   }
-  float gq[VEC], gk[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) gq[e] = gk[e] = 1.f;
-  if (g.norm && active) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if (g.q_gain != nullptr) gq[e] = g.q_gain[c0 + e];
-      if (g.k_gain != nullptr) gk[e] = g.k_gain[c0 + e];
-    }
-  }
+  const float* scales = is_v ? pg.v_scales : pg.k_scales;
 
 #pragma unroll
   for (int i = 0; i < HPG; ++i) {
     const int h = head0 + i;
-    if (h >= g.heads) break;
-    const bool is_q = h < g.Hq, is_v = h >= g.Hq + g.Hkv;
-    if (!is_q && !stored) continue;
+    if (h >= H) break;
     float u[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) u[e] = static_cast<float>(raw[i][e]);
     float rstd = 1.f;
-    if (g.norm && !is_v) {
+    if (norm) {
       float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sum = __builtin_fmaf(u[e], u[e], sum);
+      sum = row_sum<LPR>(inside ? sum : 0.f);
+      rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, g.inv_D, g.eps));
 #pragma unroll
-      for (int d = 1; d < LPR; d *= 2) sum += __shfl_xor(sum, d);
-      rstd = 1.0f / sqrtf(sum / static_cast<float>(g.D) + g.eps);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) u[e] = u[e] * rstd * (is_q ? gq[e] : gk[e]);
+      for (int e = 0; e < VEC; ++e) u[e] = u[e] * rstd * gains[e];
     }
-    if (mode != kStay && !is_v) {
+    if (turn) {
       float p[VEC];
-      if (mode == kNext) {
+      if constexpr (MODE == kNext) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) p[e] = u[e ^ 1];
-      } else if (mode == kLanes) {
-        const int step = g.pairs / VEC;
-        const int from = rl < step ? rl + step : rl - step;
+      } else if constexpr (MODE == kOpposite) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) p[e] = opposite<LPR>(u[e]);
+      } else if constexpr (MODE == kLanes) {
+        const int step = g.pairs / VEC, from = rl < step ? rl + step : rl - step;
         const int lane = static_cast<int>(threadIdx.x & 63) - rl + (from < LPR ? from : rl);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) p[e] = __shfl(u[e], lane);
-      } else {
-        const T* x = source(h);
-        const float* gain = is_q ? g.q_gain : g.k_gain;
+      } else if constexpr (MODE == kFar) {
+        const T* x = src + h * src_h - c;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          p[e] = 0.f;
-          if (active && c0 + e < R) {
-            p[e] = static_cast<float>(x[other[e]]);
-            if (g.norm) p[e] = p[e] * rstd * (gain != nullptr ? gain[other[e]] : 1.f);
-          }
+          const int ch = c0 + e, other = ch >= R ? 0 : ch < g.pairs ? ch + g.pairs : ch - g.pairs;
+          p[e] = static_cast<float>(x[other]);
+          if (norm) p[e] = p[e] * rstd * (gain != nullptr ? gain[other] : 1.f);
         }
       }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (c0 + e < R) u[e] = __builtin_fmaf(u[e], cs[e], p[e] * sn[e]);
-    }
-    if (!active) continue;
-    if (is_q) {
-      store16(static_cast<T*>(g.q_out) + t * g.qo_t + h * g.qo_h + c0, u);
-      continue;
-    }
-    const int hh = is_v ? h - g.Hq - g.Hkv : h - g.Hq;
-    if constexpr (STORE == kNoPages) {
-      store16(static_cast<T*>(g.k_out) + t * g.ko_t + hh * g.ko_h + c0, u);
-    } else {
-      const Pages& pg = g.pages;
-      const int64_t row = (static_cast<int64_t>(hh) << pg.page_log2) +
-                          (slot & ((1 << pg.page_log2) - 1));
-      char* page = static_cast<char*>(is_v ? pg.v : pg.k) +
-                   (slot >> pg.page_log2) * (is_v ? pg.v_stride : pg.k_stride);
-      if constexpr (STORE == kHalfPages) {
-        store16(reinterpret_cast<T*>(page) + row * g.D + c0, u);
-      } else {
-        const float* scales = is_v ? pg.v_scales : pg.k_scales;
-        const float inv = scales != nullptr ? 1.0f / scales[hh] : 1.f;
-        *reinterpret_cast<int2*>(page + row * g.D + c0) = codes8(u, inv);
+      for (int e = 0; e < VEC; ++e) {
+        const float v = __builtin_fmaf(u[e], cs[e], p[e] * sn[e]);
+        u[e] = MODE == kOpposite || c0 + e < R ? v : u[e];
       }
+    }
+    if (stored) {
+      if (paged && pg.coded)
+        *reinterpret_cast<int2*>(to + h * to_h) = codes8(u, scales != nullptr ? 1.0f / scales[h] : 1.f);
+      else
+        store16(reinterpret_cast<T*>(to + h * to_h), u);
     }
   }
 }
 
-template <class T, int STORE, int LPR>
+template <class T, int MODE, int LPR>
 hipError_t launch_l(HeadsArgs g, hipStream_t stream) {
-  // One head per group of lanes while that leaves lanes idle.
-  constexpr int kPer = 8;
-  const bool many = static_cast<int64_t>(g.T) * g.heads * LPR >= int64_t{kPer} * 2048 * 64;
-  g.chunks = many ? (g.heads + kPer - 1) / kPer : g.heads;
-  const int64_t groups = static_cast<int64_t>(g.T) * g.chunks;
-  const unsigned grid = static_cast<unsigned>((groups + kThreads / LPR - 1) / (kThreads / LPR));
+  // Four heads per lane share the angles and have their loads in flight together (8191
+  // tokens of 32/8 heads into codes 44 us; one head 80, two 52, eight 44; 4608 of 48: 25.5, 32,
+  // 26 and 28), where that leaves 1024 waves (1031 tokens of 24 heads: 5.6 us, one head 6.9);
+  // else one (777 tokens of 10 heads: 3.0 us, four 3.4).
+  constexpr int kPer = 4;
+  const bool many = static_cast<int64_t>(g.T) * g.heads * LPR >= int64_t{kPer} * 1024 * 64;
+  const int per = many ? kPer : 1;
+  g.q_chunks = (g.Hq + per - 1) / per;
+  g.k_chunks = (g.Hkv + per - 1) / per;
+  g.chunks = g.q_chunks + (g.slots != nullptr ? 2 : 1) * g.k_chunks;
+  g.inv_D = 1.0f / static_cast<float>(g.D);
+  const int64_t blocks = (static_cast<int64_t>(g.T) + kThreads / LPR - 1) / (kThreads / LPR) * g.chunks;
+  const unsigned grid = static_cast<unsigned>(blocks);
   if (many)
-    hipLaunchKernelGGL((heads_kernel<T, STORE, LPR, kPer>), dim3(grid), dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((heads_kernel<T, MODE, LPR, kPer>), dim3(grid), dim3(kThreads), 0, stream, g);
   else
-    hipLaunchKernelGGL((heads_kernel<T, STORE, LPR, 1>), dim3(grid), dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((heads_kernel<T, MODE, LPR, 1>), dim3(grid), dim3(kThreads), 0, stream, g);
   return hipGetLastError();
 }
 
+template <class T, int LPR>
+hipError_t launch_m(const HeadsArgs& g, hipStream_t stream) {
+  if (g.pairs == 0) return launch_l<T, kStay, LPR>(g, stream);
+  if (g.interleaved) return launch_l<T, kNext, LPR>(g, stream);
+  if (2 * g.pairs == VEC * LPR) return launch_l<T, kOpposite, LPR>(g, stream);
+  return g.pairs % VEC == 0 ? launch_l<T, kLanes, LPR>(g, stream) : launch_l<T, kFar, LPR>(g, stream);
+}
+
 template <class T>
-hipError_t launch_t(const HeadsArgs& g, int store, hipStream_t stream) {
-  if (g.D > 64)
-    return store == kNoPages     ? launch_l<T, kNoPages, 16>(g, stream)
-           : store == kHalfPages ? launch_l<T, kHalfPages, 16>(g, stream)
-                                 : launch_l<T, kCodePages, 16>(g, stream);
-  return store == kNoPages     ? launch_l<T, kNoPages, 8>(g, stream)
-         : store == kHalfPages ? launch_l<T, kHalfPages, 8>(g, stream)
-                               : launch_l<T, kCodePages, 8>(g, stream);
+hipError_t launch_t(const HeadsArgs& g, hipStream_t stream) {
+  return g.D > 64 ? launch_m<T, 16>(g, stream) : launch_m<T, 8>(g, stream);
 }
 
 // Rows back from their pages: LPR lanes per row, kPerRead heads of a token each.
@@ -301,16 +327,16 @@ hipError_t launch_rt(const ReadArgs& g, hipStream_t stream) {
 }  // namespace
 
 bool heads_fit(int64_t T, int64_t heads) {
-  return heads <= (int64_t{1} << 20) && T <= 0x7FFFFFFFll && grid_fits(T * heads / (kThreads / 16) + 1, kThreads);
+  return heads <= (int64_t{1} << 20) && T <= 0x7FFFFFFFll && grid_fits((T / (kThreads / 16) + 1) * heads, kThreads);
 }
 bool read_fits(int64_t B, int64_t L, int64_t Hkv) {
   const int64_t per = (Hkv + kPerRead - 1) / kPerRead;
   return L == 0 || (B <= (int64_t{1} << 40) / L && grid_fits(B * L * per / (kThreads / 16) + 1, kThreads));
 }
 
-hipError_t launch_heads(HeadsArgs g, int dtype, int store, hipStream_t stream) {
-  g.heads = g.Hq + (store == kNoPages ? 1 : 2) * g.Hkv;
-  return dtype == SVDQ_F16 ? launch_t<_Float16>(g, store, stream) : launch_t<__bf16>(g, store, stream);
+hipError_t launch_heads(HeadsArgs g, int dtype, hipStream_t stream) {
+  g.heads = g.Hq + (g.slots != nullptr ? 2 : 1) * g.Hkv;
+  return dtype == SVDQ_F16 ? launch_t<_Float16>(g, stream) : launch_t<__bf16>(g, stream);
 }
 
 hipError_t launch_read(ReadArgs g, int dtype, hipStream_t stream) {

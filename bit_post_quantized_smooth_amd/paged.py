@@ -15,9 +15,8 @@ import numpy as np
 
 from . import _lib, api
 from ._lib import E4M3, check, lib
-from .api import _buf, _dt_block, _dtypes, _on_gpu, _stream, _torch
+from .api import _buf, _dt_block, _on_gpu, _stream, _torch
 
-_HALVES = ("float16", "bfloat16")
 _CODES = ("uint8", "float8_e4m3fn")
 
 
@@ -57,78 +56,148 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
     raise ValueError(f"scaling: {scaling!r}, expected None, 'linear', 'base' or 'parts'")
 
 
-def _here(stream, *ts):
+# The checks run on every call and a token's kernels take no longer than they do: each
+# first tests the whole of what it requires with the cheapest accessors, and only a
+# tensor that fails is looked at piece by piece for the message.
+
+# (without torch there are no tensors to look at, and _torch() says so)
+_I32, _F32, _F64, _F16, _BF16, _CODED = (
+    getattr(_lib.torch, n, None)
+    for n in ("int32", "float32", "float64", "float16", "bfloat16", "float8_e4m3fn"))
+_U8 = getattr(_lib.torch, "uint8", None)
+
+
+def _here(stream, first, *others):
     """All tensors on one GPU, the one that the work is queued on."""
-    _on_gpu(*ts)
-    for t in ts:
-        if t is not None:
-            at = _torch().cuda.current_device() if stream is None else stream.device.index
-            if t.get_device() != at:
-                raise ValueError(f"tensors on device {t.get_device()}, the stream is on {at}")
+    at = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != at:
+            break
+    else:
+        if first.is_cuda and at == (_current_device() if stream is None else stream.device.index):
             return
+    _on_gpu(first, *others)
+    raise ValueError(f"tensors on device {at}, the stream is on "
+                     f"{_current_device() if stream is None else stream.device.index}")
+
+
+def _current_device() -> int:
+    torch = _lib.torch
+    try:
+        return torch._C._cuda_getDevice()
+    except AttributeError:                        # a torch without this name
+        return torch.cuda.current_device()
 
 
 def _rows(name, t, T, H, D, dtype):
-    """Token and head strides of a T x H x D tensor (None: any size)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    """Token and head strides of a T x H x D tensor."""
+    try:
+        if t.dtype is dtype and t.shape == (T, H, D):
+            st, sh, sd = t.stride()
+            if sd == 1:
+                # a dimension of one (or of none) is never stepped over: its stride is free
+                return st if T > 1 else 0, sh if H > 1 else 0
+    except AttributeError:
+        pass
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype is not torch.float16 and t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected float16 or bfloat16")
-    if dtype is not None and t.dtype is not dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    shape = t.shape
-    if len(shape) != 3 or (T is not None and shape[0] != T) or (H is not None and shape[1] != H) \
-            or (D is not None and shape[2] != D):
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected {(T, H, D)}")
-    st, sh, sd = t.stride()
-    n, h, d = shape
-    if d > 1 and sd != 1:
-        raise ValueError(f"{name}: the inner stride must be 1, got {sd}")
-    # a dimension of one (or of none) is never stepped over: its stride is free
-    return st if n > 1 else 0, sh if h > 1 else 0
+    if tuple(t.shape) != (T, H, D):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, H, D)}")
+    raise ValueError(f"{name}: the inner stride must be 1, got {t.stride(2)}")
 
 
-def _i32(name, t, *shape):
-    """A contiguous int32 tensor of this shape (None: any size)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+def _sizes(name, t):
+    """(tokens, heads, D, dtype) of the tensor that the others have to agree with."""
+    try:
+        T, H, D = t.shape
+        dtype = t.dtype
+        if dtype is _F16 or dtype is _BF16:
+            return T, H, D, dtype
+    except (AttributeError, ValueError):
+        pass
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype is not torch.int32:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected int32")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t
+    if t.dtype is not _F16 and t.dtype is not _BF16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected float16 or bfloat16")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (tokens, heads, channels)")
+
+
+def _flat(name, t, dtype, shape):
+    """A contiguous tensor of this type and shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _tables(t, B):
+    """(sequences, width) of the page tables; B: of that many sequences (None: any)."""
+    try:
+        shape = t.shape
+        if len(shape) == 2 and (B is None or shape[0] == B) and t.dtype is _I32 and t.is_contiguous():
+            return shape
+    except AttributeError:
+        pass
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"tables: expected a torch tensor, got {type(t).__name__}")
+    if len(t.shape) != 2 or (B is not None and t.shape[0] != B):
+        raise ValueError(f"tables: shape {tuple(t.shape)}, expected ({B}, pages)")
+    _flat("tables", t, _I32, t.shape)
 
 
 def _pool(k_pages, v_pages, k_scales, v_scales, dtype, Hkv, D):
-    """(cache dtype, pages, page size, bytes between K's pages, between V's)."""
-    torch = _torch()
-    strides = []
+    """(cache dtype, pages, page size, bytes between K's pages, between V's); Hkv None: any."""
+    kind = None
+    try:
+        shape, kind = k_pages.shape, k_pages.dtype
+        pages, heads, size, d = shape
+        kp, kh, kr, kd = k_pages.stride()
+        vp, vh, vr, vd = v_pages.stride()
+        good = ((kind is dtype or kind is _CODED or kind is _U8) and v_pages.dtype is kind and v_pages.shape == shape
+                and d == D and (Hkv is None or heads == Hkv) and kd == vd == 1 and kr == vr == d
+                and (heads < 2 or kh == vh == size * d))
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_pages(k_pages, v_pages, dtype, Hkv, D)
+    if k_scales is not None or v_scales is not None:
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None:
+                if kind is dtype:
+                    raise ValueError(f"{name}: 16-bit pages have none")
+                _flat(name, t, _F32, (heads,))
+    if pages < 2:
+        kp = vp = heads * size * d
+    if kind is dtype:
+        return _dt_block(k_pages), pages, size, 2 * kp, 2 * vp
+    return E4M3, pages, size, kp, vp
+
+
+def _refuse_pages(k_pages, v_pages, dtype, Hkv, D):
+    """Raises for the first of the two that is not pages of this type, heads and channels."""
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, _torch().Tensor):
             raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-        if t.dtype is not dtype and t.dtype not in _dtypes(_CODES):
+        if t.dtype is not dtype and t.dtype is not _CODED and t.dtype is not _U8:
             raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype} or one of {_CODES}")
-        if t.dim() != 4 or (Hkv is not None and t.shape[1] != Hkv) or (D is not None and t.shape[3] != D):
+        if t.dim() != 4 or (Hkv is not None and t.shape[1] != Hkv) or t.shape[3] != D:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (pages, {Hkv}, page size, {D})")
-        pages, heads, size, d = t.shape
-        sp, sh, ss, sd = t.stride()
-        if sd != 1 or ss != d or (heads > 1 and sh != size * d):
+        _, heads, size, d = t.shape
+        _, sh, sr, sd = t.stride()
+        if sd != 1 or sr != d or (heads > 1 and sh != size * d):
             raise ValueError(f"{name}: strides {t.stride()}, each page must be contiguous")
-        strides.append((sp if pages > 1 else heads * size * d) * t.element_size())
-    if v_pages.dtype is not k_pages.dtype or v_pages.shape != k_pages.shape:
-        raise ValueError(f"v_pages: {v_pages.dtype} {tuple(v_pages.shape)}, k_pages has {k_pages.dtype} "
-                         f"{tuple(k_pages.shape)}")
-    coded = k_pages.dtype is not dtype
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if t is not None:
-            if not coded:
-                raise ValueError(f"{name}: 16-bit pages have none")
-            _buf(name, t, api._F32, nbytes=4 * k_pages.shape[1])
-    return (E4M3 if coded else _dt_block(k_pages), k_pages.shape[0], k_pages.shape[2], *strides)
+    raise ValueError(f"v_pages: {v_pages.dtype} {tuple(v_pages.shape)}, k_pages has {k_pages.dtype} "
+                     f"{tuple(k_pages.shape)}")
 
 
 def _p(t):
@@ -137,23 +206,27 @@ def _p(t):
 
 def _rotation(T, D, positions, freqs, q_gain, k_gain, eps):
     """(pairs, eps of the library) after the checks."""
-    if (positions is None) != (freqs is None):
-        raise ValueError("positions and freqs: a rotation needs both")
     pairs = 0
-    if freqs is not None:
-        _i32("positions", positions, T)
-        _buf("freqs", freqs, ("float64",))
-        pairs = freqs.numel()
-        if freqs.dim() != 1 or 2 * pairs > D:
-            raise ValueError(f"freqs: shape {tuple(freqs.shape)}, expected up to {D // 2} pairs")
-    for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
-        if t is not None:
-            if eps is None:
-                raise ValueError(f"{name}: needs eps, without which there is no norm")
-            _buf(name, t, api._F32, nbytes=4 * D)
-    if eps is not None and not (eps >= 0 and math.isfinite(eps)):
+    if freqs is not None and positions is not None:
+        _flat("positions", positions, _I32, (T,))
+        shape = getattr(freqs, "shape", (0,))
+        pairs = shape[0] if len(shape) == 1 else D
+        if 2 * pairs > D:
+            raise ValueError(f"freqs: shape {tuple(shape)}, expected up to {D // 2} pairs")
+        _flat("freqs", freqs, _F64, (pairs,))
+    elif freqs is not None or positions is not None:
+        raise ValueError("positions and freqs: a rotation needs both")
+    if eps is None:
+        if q_gain is not None or k_gain is not None:
+            raise ValueError("q_gain and k_gain: need eps, without which there is no norm")
+        return pairs, -1.0
+    if q_gain is not None:
+        _flat("q_gain", q_gain, _F32, (D,))
+    if k_gain is not None:
+        _flat("k_gain", k_gain, _F32, (D,))
+    if not (eps >= 0 and math.isfinite(eps)):
         raise ValueError(f"eps: {eps}, expected a finite value >= 0")
-    return pairs, -1.0 if eps is None else eps
+    return pairs, eps
 
 
 def norm_rotary(Q, K, Q_out, K_out, positions=None, freqs=None, factor: float = 1.0,
@@ -167,15 +240,13 @@ def norm_rotary(Q, K, Q_out, K_out, positions=None, freqs=None, factor: float = 
     positions (int32, T) and freqs (fp64, radians per position of each pair:
     rotary_frequencies): the rotation of the first 2 * len(freqs) channels, pairs of channels
     (i, i + len(freqs)) or, ``interleaved``, (2i, 2i + 1), times ``factor``."""
-    q, qo = _rows("Q", Q, None, None, None, None), None
-    T, Hq, D = Q.shape
-    qo = _rows("Q_out", Q_out, T, Hq, D, Q.dtype)
+    T, Hq, D, dtype = _sizes("Q", Q)
+    q, qo = _rows("Q", Q, T, Hq, D, dtype), _rows("Q_out", Q_out, T, Hq, D, dtype)
     k = ko = (0, 0)
     Hkv = 0
     if K is not None or K_out is not None:
-        k = _rows("K", K, T, None, D, Q.dtype)
-        Hkv = K.shape[1]
-        ko = _rows("K_out", K_out, T, Hkv, D, Q.dtype)
+        Hkv = _sizes("K", K)[1]
+        k, ko = _rows("K", K, T, Hkv, D, dtype), _rows("K_out", K_out, T, Hkv, D, dtype)
     pairs, e = _rotation(T, D, positions, freqs, q_gain, k_gain, eps)
     _here(stream, Q, K, Q_out, K_out, positions, freqs, q_gain, k_gain)
     status = lib.svdq_norm_rotary(
@@ -194,17 +265,15 @@ def norm_rotary_write(Q, K, V, Q_out, slots, k_pages, v_pages, k_scales=None, v_
     whose slot is outside the pool, such as -1, is stored nowhere). Slots in the pool must
     differ. k_scales, v_scales (fp32, Hkv): the scales of e4m3 pages; values beyond 448 scales
     are clamped."""
-    k = _rows("K", K, None, None, None, None)
-    T, Hkv, D = K.shape
-    v = _rows("V", V, T, Hkv, D, K.dtype)
+    T, Hkv, D, dtype = _sizes("K", K)
+    k, v = _rows("K", K, T, Hkv, D, dtype), _rows("V", V, T, Hkv, D, dtype)
     q = qo = (0, 0)
     Hq = 0
     if Q is not None or Q_out is not None:
-        q = _rows("Q", Q, T, None, D, K.dtype)
-        Hq = Q.shape[1]
-        qo = _rows("Q_out", Q_out, T, Hq, D, K.dtype)
-    pool = _pool(k_pages, v_pages, k_scales, v_scales, K.dtype, Hkv, D)
-    _i32("slots", slots, T)
+        Hq = _sizes("Q", Q)[1]
+        q, qo = _rows("Q", Q, T, Hq, D, dtype), _rows("Q_out", Q_out, T, Hq, D, dtype)
+    pool = _pool(k_pages, v_pages, k_scales, v_scales, dtype, Hkv, D)
+    _flat("slots", slots, _I32, (T,))
     pairs, e = _rotation(T, D, positions, freqs, q_gain, k_gain, eps)
     _here(stream, K, V, Q, Q_out, slots, k_pages, v_pages, k_scales, v_scales, positions, freqs,
           q_gain, k_gain)
@@ -233,12 +302,12 @@ def paged_read(k_pages, v_pages, tables, lengths, K_out, V_out, k_scales=None, v
     B, L, Hkv, D = K_out.shape
     sv = api._heads("V_out", V_out, B, L, Hkv, D, K_out.dtype)
     pool = _pool(k_pages, v_pages, k_scales, v_scales, K_out.dtype, Hkv, D)
-    _i32("tables", tables, B, None)
-    _i32("lengths", lengths, B)
+    width = _tables(tables, B)[1]
+    _flat("lengths", lengths, _I32, (B,))
     _here(stream, K_out, V_out, k_pages, v_pages, tables, lengths, k_scales, v_scales)
     status = lib.svdq_paged_read(
         k_pages.data_ptr(), v_pages.data_ptr(), *pool, _p(k_scales), _p(v_scales), tables.data_ptr(),
-        tables.shape[1], lengths.data_ptr(), B, L, Hkv, D, K_out.data_ptr(), V_out.data_ptr(),
+        width, lengths.data_ptr(), B, L, Hkv, D, K_out.data_ptr(), V_out.data_ptr(),
         _dt_block(K_out), struct.pack("6q", *so, *sv), _stream(stream))
     if status:
         check(status, "svdq_paged_read")
@@ -262,19 +331,17 @@ def paged_attention(Q, k_pages, v_pages, tables, lengths, starts, Out, k_scales=
     key is 0, rows of no sequence are left as they were. With a workspace of
     paged_attention_workspace_bytes(T, B, width * page size, Hq, Hkv, D) work is split along
     the keys; calls that may run at once need one each."""
-    q = _rows("Q", Q, None, None, None, None)
-    T, Hq, D = Q.shape
-    o = _rows("Out", Out, T, Hq, D, Q.dtype)
-    pool = _pool(k_pages, v_pages, k_scales, v_scales, Q.dtype, None, D)
+    T, Hq, D, dtype = _sizes("Q", Q)
+    q, o = _rows("Q", Q, T, Hq, D, dtype), _rows("Out", Out, T, Hq, D, dtype)
+    pool = _pool(k_pages, v_pages, k_scales, v_scales, dtype, None, D)
     Hkv = k_pages.shape[1]
     if Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError(f"{Hq} query heads over {Hkv} key heads")
-    _i32("tables", tables, None, None)
-    B, width = tables.shape
-    _i32("lengths", lengths, B)
-    _i32("starts", starts, B + 1)
+    B, width = _tables(tables, None)
+    _flat("lengths", lengths, _I32, (B,))
+    _flat("starts", starts, _I32, (B + 1,))
     if slopes is not None:
-        _buf("slopes", slopes, api._F32, nbytes=4 * Hq)
+        _flat("slopes", slopes, _F32, (Hq,))
     if ws is not None:
         _buf("ws", ws, api._BYTES + api._HALF + api._F32)
     _here(stream, Q, Out, k_pages, v_pages, tables, lengths, starts, k_scales, v_scales, slopes, ws)
