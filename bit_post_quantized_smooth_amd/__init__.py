@@ -23,11 +23,11 @@ from .api import (Conv2d, Linear, Prepared, attention, attention_workspace_bytes
                   quantize_act_lowrank_down_conv_mx, quantize_act_lowrank_down_conv_tiled,
                   quantize_act_lowrank_down_mx, smoothing_factors, w4a4_gemm_lowrank_up,
                   w4a16_gemm, w4a16_tile_activation, w4a16_x_tiled_bytes, linear_w4a16)
-from .block import AttentionBlock, KeyValueCache  # noqa: F401
+from .block import AttentionBlock, KeyValueCache, PagedKeyValueCache, PageTable  # noqa: F401
 from .paged import (norm_rotary, norm_rotary_write, paged_attention,  # noqa: F401
                     paged_attention_workspace_bytes, paged_read, paged_write, rotary_frequencies)
 
-__all__ = ["AttentionBlock", "KeyValueCache", "norm_rotary", "norm_rotary_write", "paged_attention",
+__all__ = ["AttentionBlock", "KeyValueCache", "PagedKeyValueCache", "PageTable", "norm_rotary", "norm_rotary_write", "paged_attention",
            "paged_attention_workspace_bytes", "paged_read", "paged_write", "rotary_frequencies",
            "Conv2d", "Linear", "Prepared", "attention", "attention_workspace_bytes",
            "document_key_ranges", "fp8_padded", "gemm_fp8", "gemm_fp8_workspace_bytes",
