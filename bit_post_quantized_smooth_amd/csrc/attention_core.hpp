@@ -172,8 +172,10 @@ struct AttentionCore {
   }
 
   // Without a cap and slopes a score stays as the products give it and its scale
-  // goes into the exponential; with them it is made a base-2 logit here.
-  static constexpr bool RAW = CAP == kNoCap && !SLOPES;
+  // goes into the exponential; with them it is made a base-2 logit here. (With HOLES
+  // slopes too leave it so: slope2 is then in the scores' units, and the distance of a
+  // key is one subtraction of whole numbers in fp32.)
+  static constexpr bool RAW = CAP == kNoCap && (!SLOPES || HOLES);
 
   // x = K Q^T of the 32 keys from LDS row `row0` on; at: the stage's base address
   __device__ __forceinline__ v16f products(int at, int row0) {
@@ -211,6 +213,7 @@ struct AttentionCore {
   template <bool MASK>
   __device__ __forceinline__ float logits(v16f& x, int key0, uint32_t gone) {
     float top = kNegInf;
+    const float away = SLOPES && HOLES ? static_cast<float>(pos - key0 - 4 * h) : 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int key = key0 + (i & 3) + 8 * (i >> 2) + 4 * h;
@@ -221,10 +224,12 @@ struct AttentionCore {
         v = __builtin_fmaf(-2.0f * g.cap2, __builtin_amdgcn_rcpf(e + 1.0f), g.cap2);
       } else if constexpr (CAP == kAnyCap) {
         v = any_cap(v);
-      } else if constexpr (SLOPES) {
+      } else if constexpr (SLOPES && !HOLES) {
         v = v * g.scale2;
       }
-      if constexpr (SLOPES)
+      if constexpr (SLOPES && HOLES)
+        v = __builtin_fmaf(-slope2, fabsf(away - static_cast<float>((i & 3) + 8 * (i >> 2))), v);
+      else if constexpr (SLOPES)
         v = __builtin_fmaf(-slope2, fabsf(static_cast<float>(pos - key)), v);
       if constexpr (MASK) v = static_cast<uint32_t>(key - lo) < width ? v : kNegInf;
       if constexpr (MASK && HOLES) v = (gone >> (i >> 3) & 1) != 0 ? kNegInf : v;
