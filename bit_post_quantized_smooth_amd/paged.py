@@ -14,8 +14,8 @@ import struct
 import numpy as np
 
 from . import _lib, api
-from ._lib import E4M3, check, lib
-from .api import _buf, _dt_block, _on_gpu, _stream, _torch
+from ._lib import BF16, E4M3, F16, check, lib
+from .api import _buf, _on_gpu, _torch
 
 _CODES = ("uint8", "float8_e4m3fn")
 
@@ -65,63 +65,67 @@ _I32, _F32, _F64, _F16, _BF16, _CODED = (
     getattr(_lib.torch, n, None)
     for n in ("int32", "float32", "float64", "float16", "bfloat16", "float8_e4m3fn"))
 _U8 = getattr(_lib.torch, "uint8", None)
+_eight, _six, _four = (struct.Struct(f"{n}q").pack for n in (8, 6, 4))
 
 
-def _here(stream, first, *others):
-    """All tensors on one GPU, the one that the work is queued on."""
+_device = getattr(getattr(_lib.torch, "_C", None), "_cuda_getDevice", None)
+_raw_stream = getattr(getattr(_lib.torch, "_C", None), "_cuda_getCurrentRawStream", None)
+if _device is None or _raw_stream is None:        # a torch without these names
+    def _device():
+        return _torch().cuda.current_device()
+
+    def _raw_stream(device):
+        return _torch().cuda.current_stream(device).cuda_stream
+
+
+def _queue(stream, first, *others):
+    """The handle of the stream that the work goes to, all tensors being on its GPU."""
     at = first.get_device()
     for t in others:
         if t is not None and t.get_device() != at:
             break
     else:
-        if first.is_cuda and at == (_current_device() if stream is None else stream.device.index):
-            return
+        if at >= 0:
+            if stream is None:
+                if at == _device():
+                    return _raw_stream(at)
+            elif at == stream.device.index:
+                return stream.cuda_stream
     _on_gpu(first, *others)
     raise ValueError(f"tensors on device {at}, the stream is on "
-                     f"{_current_device() if stream is None else stream.device.index}")
+                     f"{_device() if stream is None else stream.device.index}")
 
 
-def _current_device() -> int:
-    torch = _lib.torch
-    try:
-        return torch._C._cuda_getDevice()
-    except AttributeError:                        # a torch without this name
-        return torch.cuda.current_device()
-
-
-def _rows(name, t, T, H, D, dtype):
-    """Token and head strides of a T x H x D tensor."""
-    try:
-        if t.dtype is dtype and t.shape == (T, H, D):
-            st, sh, sd = t.stride()
-            if sd == 1:
-                # a dimension of one (or of none) is never stepped over: its stride is free
-                return st if T > 1 else 0, sh if H > 1 else 0
-    except AttributeError:
-        pass
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != (T, H, D):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, H, D)}")
-    raise ValueError(f"{name}: the inner stride must be 1, got {t.stride(2)}")
-
-
-def _sizes(name, t):
-    """(tokens, heads, D, dtype) of the tensor that the others have to agree with."""
-    try:
-        T, H, D = t.shape
-        dtype = t.dtype
-        if dtype is _F16 or dtype is _BF16:
-            return T, H, D, dtype
-    except (AttributeError, ValueError):
-        pass
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype is not _F16 and t.dtype is not _BF16:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected float16 or bfloat16")
-    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (tokens, heads, channels)")
+def _refuse_heads(first, second, positions, freqs, slots=None):
+    """Raises for the first thing wrong with tensors of heads, (name, tensor) each: `first` of
+    one shape T x H x D and type, `second` of another H; with a rotation and slots of T."""
+    torch = _torch()
+    T = D = dtype = None
+    for some in (first, second):
+        H = None
+        for name, t in some:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+            if t.dtype is not _F16 and t.dtype is not _BF16:
+                raise ValueError(f"{name}: dtype {t.dtype}, expected float16 or bfloat16")
+            if dtype is not None and t.dtype is not dtype:
+                raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+            shape = tuple(t.shape)
+            if len(shape) != 3 or any(n is not None and n != m for n, m in zip((T, H, D), shape)):
+                raise ValueError(f"{name}: shape {shape}, expected {(T, H, D)}")
+            (T, H, D), dtype = shape, t.dtype
+            if t.stride(2) != 1:
+                raise ValueError(f"{name}: the inner stride must be 1, got {t.stride(2)}")
+    if slots is not None:
+        _flat("slots", slots, _I32, (T,))
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs: a rotation needs both")
+    if freqs is not None:
+        _flat("positions", positions, _I32, (T,))
+        shape = tuple(getattr(freqs, "shape", ()))
+        if len(shape) != 1 or 2 * shape[0] > D:
+            raise ValueError(f"freqs: shape {shape}, expected up to {D // 2} pairs")
+        _flat("freqs", freqs, _F64, shape)
 
 
 def _flat(name, t, dtype, shape):
@@ -179,7 +183,7 @@ def _pool(k_pages, v_pages, k_scales, v_scales, dtype, Hkv, D):
     if pages < 2:
         kp = vp = heads * size * d
     if kind is dtype:
-        return _dt_block(k_pages), pages, size, 2 * kp, 2 * vp
+        return BF16 if kind is _BF16 else F16, pages, size, 2 * kp, 2 * vp
     return E4M3, pages, size, kp, vp
 
 
@@ -200,33 +204,15 @@ def _refuse_pages(k_pages, v_pages, dtype, Hkv, D):
                      f"{tuple(k_pages.shape)}")
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-def _rotation(T, D, positions, freqs, q_gain, k_gain, eps):
-    """(pairs, eps of the library) after the checks."""
-    pairs = 0
-    if freqs is not None and positions is not None:
-        _flat("positions", positions, _I32, (T,))
-        shape = getattr(freqs, "shape", (0,))
-        pairs = shape[0] if len(shape) == 1 else D
-        if 2 * pairs > D:
-            raise ValueError(f"freqs: shape {tuple(shape)}, expected up to {D // 2} pairs")
-        _flat("freqs", freqs, _F64, (pairs,))
-    elif freqs is not None or positions is not None:
-        raise ValueError("positions and freqs: a rotation needs both")
-    if eps is None:
-        if q_gain is not None or k_gain is not None:
-            raise ValueError("q_gain and k_gain: need eps, without which there is no norm")
-        return pairs, -1.0
+def _norm(eps, q_gain, k_gain, D):
+    """eps after the checks of the norm."""
     if q_gain is not None:
         _flat("q_gain", q_gain, _F32, (D,))
     if k_gain is not None:
         _flat("k_gain", k_gain, _F32, (D,))
     if not (eps >= 0 and math.isfinite(eps)):
         raise ValueError(f"eps: {eps}, expected a finite value >= 0")
-    return pairs, eps
+    return eps
 
 
 def norm_rotary(Q, K, Q_out, K_out, positions=None, freqs=None, factor: float = 1.0,
@@ -240,19 +226,53 @@ def norm_rotary(Q, K, Q_out, K_out, positions=None, freqs=None, factor: float = 
     positions (int32, T) and freqs (fp64, radians per position of each pair:
     rotary_frequencies): the rotation of the first 2 * len(freqs) channels, pairs of channels
     (i, i + len(freqs)) or, ``interleaved``, (2i, 2i + 1), times ``factor``."""
-    T, Hq, D, dtype = _sizes("Q", Q)
-    q, qo = _rows("Q", Q, T, Hq, D, dtype), _rows("Q_out", Q_out, T, Hq, D, dtype)
-    k = ko = (0, 0)
-    Hkv = 0
-    if K is not None or K_out is not None:
-        Hkv = _sizes("K", K)[1]
-        k, ko = _rows("K", K, T, Hkv, D, dtype), _rows("K_out", K_out, T, Hkv, D, dtype)
-    pairs, e = _rotation(T, D, positions, freqs, q_gain, k_gain, eps)
-    _here(stream, Q, K, Q_out, K_out, positions, freqs, q_gain, k_gain)
+    try:
+        T, Hq, D = shape = Q.shape
+        dtype = Q.dtype
+        qt, qh, qd = Q.stride()
+        ot, oh, od = Q_out.stride()
+        good = (Q_out.shape == shape and Q_out.dtype is dtype and (dtype is _F16 or dtype is _BF16)
+                and qd == od == 1)
+        Hkv = kt = kh = nt = nh = pairs = 0
+        if K is not None or K_out is not None:
+            Tk, Hkv, Dk = shape = K.shape
+            kt, kh, kd = K.stride()
+            nt, nh, nd = K_out.stride()
+            good = (good and Tk == T and Dk == D and K.dtype is dtype and K_out.dtype is dtype
+                    and K_out.shape == shape and kd == nd == 1)
+        if freqs is not None:
+            pairs, = freqs.shape
+            good = (good and 2 * pairs <= D and freqs.dtype is _F64 and freqs.is_contiguous()
+                    and positions.dtype is _I32 and positions.shape == (T,) and positions.is_contiguous())
+        elif positions is not None:
+            good = False
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_heads((("Q", Q), ("Q_out", Q_out)),
+                      () if K is None and K_out is None else (("K", K), ("K_out", K_out)),
+                      positions, freqs)
+    # a dimension of one (or of none) is never stepped over: its stride is free
+    if T < 2:
+        qt = ot = kt = nt = 0
+    if Hq < 2:
+        qh = oh = 0
+    if Hkv < 2:
+        kh = nh = 0
+    if eps is None:
+        e = -1.0
+        if q_gain is not None or k_gain is not None:
+            raise ValueError("q_gain and k_gain: need eps, without which there is no norm")
+    else:
+        e = _norm(eps, q_gain, k_gain, D)
+    queue = _queue(stream, Q, K, Q_out, K_out, positions, freqs, q_gain, k_gain)
     status = lib.svdq_norm_rotary(
-        Q.data_ptr(), _p(K), Q_out.data_ptr(), _p(K_out), _dt_block(Q), T, Hq, Hkv, D,
-        struct.pack("8q", *q, *k, *qo, *ko), _p(positions), _p(freqs), pairs, factor,
-        1 if interleaved else 0, _p(q_gain), _p(k_gain), e, _stream(stream))
+        Q.data_ptr(), None if K is None else K.data_ptr(), Q_out.data_ptr(),
+        None if K_out is None else K_out.data_ptr(), BF16 if dtype is _BF16 else F16, T, Hq, Hkv, D,
+        _eight(qt, qh, kt, kh, ot, oh, nt, nh), None if freqs is None else positions.data_ptr(),
+        None if freqs is None else freqs.data_ptr(), pairs, factor, 1 if interleaved else 0,
+        None if q_gain is None else q_gain.data_ptr(), None if k_gain is None else k_gain.data_ptr(),
+        e, queue)
     if status:
         check(status, "svdq_norm_rotary")
 
@@ -265,23 +285,56 @@ def norm_rotary_write(Q, K, V, Q_out, slots, k_pages, v_pages, k_scales=None, v_
     whose slot is outside the pool, such as -1, is stored nowhere). Slots in the pool must
     differ. k_scales, v_scales (fp32, Hkv): the scales of e4m3 pages; values beyond 448 scales
     are clamped."""
-    T, Hkv, D, dtype = _sizes("K", K)
-    k, v = _rows("K", K, T, Hkv, D, dtype), _rows("V", V, T, Hkv, D, dtype)
-    q = qo = (0, 0)
-    Hq = 0
-    if Q is not None or Q_out is not None:
-        Hq = _sizes("Q", Q)[1]
-        q, qo = _rows("Q", Q, T, Hq, D, dtype), _rows("Q_out", Q_out, T, Hq, D, dtype)
+    try:
+        T, Hkv, D = shape = K.shape
+        dtype = K.dtype
+        kt, kh, kd = K.stride()
+        vt, vh, vd = V.stride()
+        good = (V.shape == shape and V.dtype is dtype and (dtype is _F16 or dtype is _BF16) and kd == vd == 1
+                and slots.dtype is _I32 and slots.shape == (T,) and slots.is_contiguous())
+        Hq = qt = qh = ot = oh = pairs = 0
+        if Q is not None or Q_out is not None:
+            Tq, Hq, Dq = shape = Q.shape
+            qt, qh, qd = Q.stride()
+            ot, oh, od = Q_out.stride()
+            good = (good and Tq == T and Dq == D and Q.dtype is dtype and Q_out.dtype is dtype
+                    and Q_out.shape == shape and qd == od == 1)
+        if freqs is not None:
+            pairs, = freqs.shape
+            good = (good and 2 * pairs <= D and freqs.dtype is _F64 and freqs.is_contiguous()
+                    and positions.dtype is _I32 and positions.shape == (T,) and positions.is_contiguous())
+        elif positions is not None:
+            good = False
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_heads((("K", K), ("V", V)),
+                      () if Q is None and Q_out is None else (("Q", Q), ("Q_out", Q_out)),
+                      positions, freqs, slots)
+    if T < 2:
+        kt = vt = qt = ot = 0
+    if Hkv < 2:
+        kh = vh = 0
+    if Hq < 2:
+        qh = oh = 0
     pool = _pool(k_pages, v_pages, k_scales, v_scales, dtype, Hkv, D)
-    _flat("slots", slots, _I32, (T,))
-    pairs, e = _rotation(T, D, positions, freqs, q_gain, k_gain, eps)
-    _here(stream, K, V, Q, Q_out, slots, k_pages, v_pages, k_scales, v_scales, positions, freqs,
-          q_gain, k_gain)
+    if eps is None:
+        e = -1.0
+        if q_gain is not None or k_gain is not None:
+            raise ValueError("q_gain and k_gain: need eps, without which there is no norm")
+    else:
+        e = _norm(eps, q_gain, k_gain, D)
+    queue = _queue(stream, K, V, Q, Q_out, slots, k_pages, v_pages, k_scales, v_scales, positions,
+                   freqs, q_gain, k_gain)
     status = lib.svdq_paged_write(
-        _p(Q), K.data_ptr(), V.data_ptr(), _p(Q_out), _dt_block(K), T, Hq, Hkv, D,
-        struct.pack("8q", *q, *k, *v, *qo), _p(positions), _p(freqs), pairs, factor,
-        1 if interleaved else 0, _p(q_gain), _p(k_gain), e, slots.data_ptr(), k_pages.data_ptr(),
-        v_pages.data_ptr(), *pool, _p(k_scales), _p(v_scales), _stream(stream))
+        None if Q is None else Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+        None if Q_out is None else Q_out.data_ptr(), BF16 if dtype is _BF16 else F16, T, Hq, Hkv, D,
+        _eight(qt, qh, kt, kh, vt, vh, ot, oh), None if freqs is None else positions.data_ptr(),
+        None if freqs is None else freqs.data_ptr(), pairs, factor, 1 if interleaved else 0,
+        None if q_gain is None else q_gain.data_ptr(), None if k_gain is None else k_gain.data_ptr(),
+        e, slots.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), *pool,
+        None if k_scales is None else k_scales.data_ptr(),
+        None if v_scales is None else v_scales.data_ptr(), queue)
     if status:
         check(status, "svdq_paged_write")
 
@@ -298,17 +351,37 @@ def paged_read(k_pages, v_pages, tables, lengths, K_out, V_out, k_scales=None, v
     tables[b] (int32, B x width) into K_out and V_out (B x L x Hkv x D, fp16 or bf16; of 16-bit
     pages the same type), codes times their scales. Rows behind a sequence's length are left as
     they were."""
-    so = api._heads("K_out", K_out, None, None, None, None, None)
-    B, L, Hkv, D = K_out.shape
-    sv = api._heads("V_out", V_out, B, L, Hkv, D, K_out.dtype)
-    pool = _pool(k_pages, v_pages, k_scales, v_scales, K_out.dtype, Hkv, D)
-    width = _tables(tables, B)[1]
-    _flat("lengths", lengths, _I32, (B,))
-    _here(stream, K_out, V_out, k_pages, v_pages, tables, lengths, k_scales, v_scales)
+    try:
+        B, L, Hkv, D = shape = K_out.shape
+        dtype = K_out.dtype
+        kb, kt, kh, kd = K_out.stride()
+        vb, vt, vh, vd = V_out.stride()
+        rows, width = tables.shape
+        good = (V_out.shape == shape and V_out.dtype is dtype and (dtype is _F16 or dtype is _BF16)
+                and kd == vd == 1 and rows == B and tables.dtype is _I32 and tables.is_contiguous()
+                and lengths.dtype is _I32 and lengths.shape == (B,) and lengths.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        api._heads("K_out", K_out, None, None, None, None, None)
+        api._heads("V_out", V_out, *K_out.shape, K_out.dtype)
+        _tables(tables, K_out.shape[0])
+        _flat("lengths", lengths, _I32, (K_out.shape[0],))
+    # a dimension of one (or of none) is never stepped over: its stride is free
+    if B < 2:
+        kb = vb = 0
+    if L < 2:
+        kt = vt = 0
+    if Hkv < 2:
+        kh = vh = 0
+    pool = _pool(k_pages, v_pages, k_scales, v_scales, dtype, Hkv, D)
+    queue = _queue(stream, K_out, V_out, k_pages, v_pages, tables, lengths, k_scales, v_scales)
     status = lib.svdq_paged_read(
-        k_pages.data_ptr(), v_pages.data_ptr(), *pool, _p(k_scales), _p(v_scales), tables.data_ptr(),
-        width, lengths.data_ptr(), B, L, Hkv, D, K_out.data_ptr(), V_out.data_ptr(),
-        _dt_block(K_out), struct.pack("6q", *so, *sv), _stream(stream))
+        k_pages.data_ptr(), v_pages.data_ptr(), *pool,
+        None if k_scales is None else k_scales.data_ptr(),
+        None if v_scales is None else v_scales.data_ptr(), tables.data_ptr(), width,
+        lengths.data_ptr(), B, L, Hkv, D, K_out.data_ptr(), V_out.data_ptr(),
+        BF16 if dtype is _BF16 else F16, _six(kb, kt, kh, vb, vt, vh), queue)
     if status:
         check(status, "svdq_paged_read")
 
@@ -331,25 +404,44 @@ def paged_attention(Q, k_pages, v_pages, tables, lengths, starts, Out, k_scales=
     key is 0, rows of no sequence are left as they were. With a workspace of
     paged_attention_workspace_bytes(T, B, width * page size, Hq, Hkv, D) work is split along
     the keys; calls that may run at once need one each."""
-    T, Hq, D, dtype = _sizes("Q", Q)
-    q, o = _rows("Q", Q, T, Hq, D, dtype), _rows("Out", Out, T, Hq, D, dtype)
+    try:
+        T, Hq, D = shape = Q.shape
+        dtype = Q.dtype
+        qt, qh, qd = Q.stride()
+        ot, oh, od = Out.stride()
+        B, width = tables.shape
+        good = (Out.shape == shape and Out.dtype is dtype and (dtype is _F16 or dtype is _BF16)
+                and qd == od == 1 and tables.dtype is _I32 and tables.is_contiguous()
+                and lengths.dtype is _I32 and lengths.shape == (B,) and lengths.is_contiguous()
+                and starts.dtype is _I32 and starts.shape == (B + 1,) and starts.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_heads((("Q", Q), ("Out", Out)), (), None, None)
+        B, width = _tables(tables, None)
+        _flat("lengths", lengths, _I32, (B,))
+        _flat("starts", starts, _I32, (B + 1,))
+    if T < 2:
+        qt = ot = 0
+    if Hq < 2:
+        qh = oh = 0
     pool = _pool(k_pages, v_pages, k_scales, v_scales, dtype, None, D)
     Hkv = k_pages.shape[1]
     if Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError(f"{Hq} query heads over {Hkv} key heads")
-    B, width = _tables(tables, None)
-    _flat("lengths", lengths, _I32, (B,))
-    _flat("starts", starts, _I32, (B + 1,))
     if slopes is not None:
         _flat("slopes", slopes, _F32, (Hq,))
     if ws is not None:
         _buf("ws", ws, api._BYTES + api._HALF + api._F32)
-    _here(stream, Q, Out, k_pages, v_pages, tables, lengths, starts, k_scales, v_scales, slopes, ws)
+    queue = _queue(stream, Q, Out, k_pages, v_pages, tables, lengths, starts, k_scales, v_scales, slopes,
+                   ws)
     status = lib.svdq_paged_attention(
-        Q.data_ptr(), Out.data_ptr(), _dt_block(Q), T, Hq, Hkv, D, struct.pack("4q", *q, *o),
-        k_pages.data_ptr(), v_pages.data_ptr(), *pool, _p(k_scales), _p(v_scales), tables.data_ptr(),
-        width, lengths.data_ptr(), starts.data_ptr(), B, D ** -0.5 if scale is None else scale,
-        softcap, _p(slopes), 1 if causal else 0, _p(ws), 0 if ws is None else ws.nbytes,
-        _stream(stream))
+        Q.data_ptr(), Out.data_ptr(), BF16 if dtype is _BF16 else F16, T, Hq, Hkv, D,
+        _four(qt, qh, ot, oh), k_pages.data_ptr(), v_pages.data_ptr(), *pool,
+        None if k_scales is None else k_scales.data_ptr(),
+        None if v_scales is None else v_scales.data_ptr(), tables.data_ptr(), width,
+        lengths.data_ptr(), starts.data_ptr(), B, D ** -0.5 if scale is None else scale, softcap,
+        None if slopes is None else slopes.data_ptr(), 1 if causal else 0,
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, queue)
     if status:
         check(status, "svdq_paged_attention")
