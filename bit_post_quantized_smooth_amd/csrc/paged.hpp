@@ -42,6 +42,7 @@ struct HeadsArgs {
   int T, Hq, Hkv, D;
   int heads, q_chunks, k_chunks, chunks;   // set by launch_heads
   float inv_D;
+  int most_unit;
 };
 
 // Whether one launch covers T tokens of this many heads.

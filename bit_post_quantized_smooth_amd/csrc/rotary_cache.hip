@@ -19,6 +19,9 @@
 // their loads are in flight together.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "../../include/svdq.h"
 #include "block_common.hpp"
 #include "block_launch.hpp"
@@ -61,6 +64,14 @@ __device__ __forceinline__ float row_sum(float x) {
   x += dpp<0x4E, 0xF>(x, x);
   x += dpp<0x141, 0xF>(x, x);
   if constexpr (LPR == 16) x += dpp<0x140, 0xF>(x, x);
+  return x;
+}
+template <int LPR>
+__device__ __forceinline__ float row_max(float x) {
+  x = fmaxf(x, dpp<0xB1, 0xF>(x, x));
+  x = fmaxf(x, dpp<0x4E, 0xF>(x, x));
+  x = fmaxf(x, dpp<0x141, 0xF>(x, x));
+  if constexpr (LPR == 16) x = fmaxf(x, dpp<0x140, 0xF>(x, x));
   return x;
 }
 
@@ -183,8 +194,26 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs g) {
       float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sum = __builtin_fmaf(u[e], u[e], sum);
-      sum = row_sum<LPR>(inside ? sum : 0.f);
-      rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, g.inv_D, g.eps));
+      float mean = __builtin_fmaf(row_sum<LPR>(inside ? sum : 0.f), g.inv_D, g.eps);
+      float unit = 1.f;
+      // squares beyond fp32 (bf16 values above 2^63) or below it (with an eps as small):
+      // of values in units of the row's largest
+      const bool far = !(mean >= 0x1p-100f && mean < __builtin_inff());
+      if (__builtin_amdgcn_ballot_w64(far) != 0) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) top = fmaxf(top, fabsf(u[e]));
+        top = row_max<LPR>(inside ? top : 0.f);
+        if (far && top > 0.f && top < __builtin_inff()) {
+          unit = __builtin_ldexpf(1.f, min(max(-__builtin_amdgcn_frexp_expf(top), -126), g.most_unit));
+          sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) sum = __builtin_fmaf(u[e] * unit, u[e] * unit, sum);
+        }
+        sum = row_sum<LPR>(inside ? sum : 0.f);
+        if (unit != 1.f) mean = __builtin_fmaf(sum, g.inv_D, g.eps * unit * unit);
+      }
+      rstd = __builtin_amdgcn_rsqf(mean) * unit;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) u[e] = u[e] * rstd * gains[e];
     }
@@ -238,6 +267,7 @@ hipError_t launch_l(HeadsArgs g, hipStream_t stream) {
   g.k_chunks = (g.Hkv + per - 1) / per;
   g.chunks = g.q_chunks + (g.slots != nullptr ? 2 : 1) * g.k_chunks;
   g.inv_D = 1.0f / static_cast<float>(g.D);
+  g.most_unit = g.eps > 0.f ? std::min(126, (100 - std::ilogb(g.eps)) / 2) : 126;   // eps * 2^(2 unit) stays finite
   const int64_t blocks = (static_cast<int64_t>(g.T) + kThreads / LPR - 1) / (kThreads / LPR) * g.chunks;
   const unsigned grid = static_cast<unsigned>(blocks);
   if (many)

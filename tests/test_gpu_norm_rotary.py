@@ -146,6 +146,16 @@ def test_infinities_and_nan_stay_in_their_head(sq):
     assert not rows[1, 2] and int((~rows).sum()) == 3
 
 
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_norms_of_very_large_and_small_values(sq, D):
+    """bf16 rows whose squares leave fp32: the norm is that of the formula, beside ordinary rows."""
+    q = heads(8, 3, D, BF16)
+    for i, x in enumerate((1e30, 3e38 / 8, 1e-25, 1.0, 1e19, 1e-37, 1e10, 1e-12)):
+        q[i, 1] = (q[i, 1].float() * x).to(BF16)
+    for eps in (0.0, 1e-6):
+        check(sq, q, None, eps=eps)
+
+
 def test_zero_rows(sq):
     q = torch.zeros(3, 2, 64, dtype=F16, device="cuda")
     out = torch.full_like(q, 5.0)
