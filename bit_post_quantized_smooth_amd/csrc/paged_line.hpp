@@ -103,12 +103,14 @@ __device__ __forceinline__ int quotient(int64_t a, int64_t b, int64_t& left) {
   return q;
 }
 
-// The sequences 64 at a time, one a lane, with the work up to each one's end. Up to 64
-// are looked at once.
+// The line as a wave sees it. Each lane sums up `span` sequences, one after the other (one
+// each where there are up to 64: 1000 take 4 rounds of loads instead of 16), and 64 of
+// them are held at a time, one a lane.
 struct Line {
   Sequence own;
-  int64_t upto;
   int at;                                 // the first of those held
+  int span;
+  int64_t upto;                           // work of the lanes' sequences up to this lane's end
   int64_t per_head;                       // work of one key head
 
   __device__ __forceinline__ void hold(const PagedArgs& g, int first) {
@@ -116,18 +118,28 @@ struct Line {
     const int b = first + static_cast<int>(threadIdx.x & 63);
     own = sequence(g, b < g.B ? b : g.B - 1);
     if (b >= g.B) own.tiles = 0;
-    upto = running_sum(own.before(own.tiles));
   }
   __device__ __forceinline__ Line(const PagedArgs& g) {
-    per_head = 0;
-    for (int b0 = 0; b0 < g.B; b0 += 64) {
-      hold(g, b0);
-      per_head += of_lane(upto, 63);
+    span = (g.B + 63) / 64;
+    int64_t sum = 0;
+    if (span == 1) {
+      hold(g, 0);
+      sum = own.before(own.tiles);
+    } else {
+      at = -64;                           // none
+      const int b0 = static_cast<int>(threadIdx.x & 63) * span;
+#pragma unroll 4
+      for (int i = 0; i < span; ++i) {
+        const Sequence s = sequence(g, min(b0 + i, g.B - 1));
+        if (b0 + i < g.B) sum += s.before(s.tiles);
+      }
     }
+    upto = running_sum(sum);
+    per_head = of_lane(upto, 63);
   }
   // Sequence b, the same for the whole wave.
   __device__ __forceinline__ Sequence get(const PagedArgs& g, int b) {
-    if (b < at || b >= at + 64) hold(g, b & ~63);
+    if (b < at || b >= at + 64) hold(g, b);
     const int lane = b - at;
     Sequence s;
     s.first = __builtin_amdgcn_readlane(own.first, lane);
@@ -143,21 +155,30 @@ struct Place {
   int hk, b, r;
   int64_t start;                          // the tile's
 };
+// The first lane whose sum exceeds left, which is taken on from there.
+__device__ __forceinline__ int lane_of(int64_t upto, int64_t& left) {
+  const uint64_t behind = __builtin_amdgcn_ballot_w64(upto > left);
+  const int lane = behind != 0 ? __builtin_ctzll(behind) : 63;
+  if (lane > 0) left -= of_lane(upto, lane - 1);
+  return lane;
+}
 __device__ __forceinline__ Place place(const PagedArgs& g, Line& line, int64_t c, Sequence& s) {
   Place p;
   int64_t left;
   p.hk = quotient(c, line.per_head, left);
-  p.b = 0;
-  for (int b0 = 0; b0 < g.B; b0 += 64) {
-    if (line.at != b0) line.hold(g, b0);
-    const uint64_t behind = __builtin_amdgcn_ballot_w64(line.upto > left);
-    if (behind != 0) {
-      const int at = __builtin_ctzll(behind);
-      if (at > 0) left -= of_lane(line.upto, at - 1);
-      p.b = b0 + at;
-      break;
+  p.b = lane_of(line.upto, left) * line.span;
+  if (line.span > 1) {
+    while (true) {
+      line.hold(g, p.b);
+      const int64_t upto = running_sum(line.own.before(line.own.tiles));
+      const int64_t all = of_lane(upto, 63);
+      if (all > left || p.b + 64 >= g.B) {
+        p.b += lane_of(upto, left);
+        break;
+      }
+      left -= all;
+      p.b += 64;
     }
-    left -= of_lane(line.upto, 63);
   }
   s = line.get(g, p.b);
   int lo = 0, hi = s.tiles - 1;           // the last tile that starts at or before left

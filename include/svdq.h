@@ -834,7 +834,8 @@ size_t svdq_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t capaci
  * Keys and values are the pages' values or codes. A row that sees no key is 0; a key
  * that a row does not see does not reach its output whatever its page holds. Rows of
  * no sequence are left as they were. strides: (token, head) of Q and Out, which may not
- * overlap. T * Hq: up to 2^30. ws: NULL or a 16-byte aligned workspace; with at least
+ * overlap. T * Hq: up to 2^30; width * page_size: up to 2^26; Hq / Hkv: up to 256; scale:
+ * with slopes 0 or at least 2^-40. ws: NULL or a 16-byte aligned workspace; with at least
  * svdq_paged_attention_workspace_bytes bytes work is split along the keys. Two calls
  * that may run at once need a workspace each. */
 int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t Hq, int64_t Hkv,

@@ -11,6 +11,7 @@ import block_ref as R
 F64 = R.F64
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
 E4M3 = torch.float8_e4m3fn
+VALUES = torch.from_numpy(R.e4m3_values())
 
 
 def half_step(dtype):
@@ -147,10 +148,16 @@ class Pool:
         there = (ids >= 0) & (ids < self.k.shape[0])
         ids = torch.where(there, ids, 0)
         for x, s in ((self.k, self.ks), (self.v, self.vs)):
-            x = R.decode(x) if self.coded else x.cpu().to(F64)
+            if x.shape[0] == 0:
+                out.append(torch.zeros(n, x.shape[1], x.shape[3], dtype=F64))
+                continue
+            # the sequence's pages first: pools are large
+            used, where = torch.unique(ids, return_inverse=True)
+            x = (x.view(torch.uint8) if self.coded else x)[used.to(x.device)]
+            x = VALUES[x.cpu().long()] if self.coded else x.cpu().to(F64)
             if s is not None:
                 x = x * s.cpu().to(F64).view(-1, 1, 1)
-            out.append(x[ids, :, torch.arange(n) % self.page] if x.shape[0] else torch.zeros(n, *x.shape[1::2], dtype=F64))
+            out.append(x[where, :, torch.arange(n) % self.page])
         return (*out, there)
 
 

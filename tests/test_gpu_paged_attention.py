@@ -143,6 +143,25 @@ def test_more_sequences_than_a_wave(sq):
     check(sq, queries(sum(new), 4, 64, BF16), p, starts_of(new))
 
 
+@pytest.mark.parametrize("B", [65, 130, 1000, 4200])
+def test_large_batches(sq, B):
+    """Single tokens of many short sequences, some empty, and two chunks among them."""
+    held = [(11 * i) % 23 for i in range(B)]
+    new = [1 if h and i % 9 else 0 for i, h in enumerate(held)]
+    held[B // 2], new[B // 2], held[B - 1], new[B - 1] = 1500, 1, 300, 40
+    p = P.Pool(held, 1, 64, BF16, True, 16).cuda()
+    check(sq, queries(sum(new), 2, 64, BF16), p, starts_of(new))
+
+
+def test_a_workspace_too_small_is_not_used(sq):
+    p = P.Pool([3000, 900], 2, 64, F16, True, 64).cuda()
+    q, s = queries(2, 4, 64, F16), torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    out, ws = torch.empty_like(q), torch.full((1024,), 0x5A, dtype=torch.uint8, device="cuda")
+    assert sq.paged_attention_workspace_bytes(2, 2, p.width * 64, 4, 2, 64) > 1024
+    sq.paged_attention(q, p.k, p.v, p.tables, p.lengths, s, out, p.ks, p.vs, ws=ws)
+    assert torch.equal(out, run(sq, q, p, [0, 1, 2], ws=False)) and bool((ws == 0x5A).all())
+
+
 @pytest.mark.parametrize("n", [1, 150])
 def test_pages_outside_the_pool_are_not_seen(sq, kind, n):
     dtype, coded = kind

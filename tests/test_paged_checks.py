@@ -202,13 +202,13 @@ def test_c_read_refuses_on_the_host():
 
 
 def attn(Q=P, Out=P, dt=1, t=4, Hq=2, Hkv=1, d=64, st=None, cd=4, size=16, pages=5, tb=P, width=3, ln=P, sr=P, B=2, scale=1.0,
-         cap=0.0, ws=None):
+         cap=0.0, ws=None, slopes=None):
     s = [Hq * d, d, Hq * d, d]
     for i, x in (st or {}).items():
         s[i] = x
     page = size * Hkv * d * 2
     return _lib.lib.svdq_paged_attention(Q, Out, dt, t, Hq, Hkv, d, strides(*s), P, P, cd, pages, size, page, page, None, None, tb,
-                                         width, ln, sr, B, scale, cap, None, 1, ws, 0, None)
+                                         width, ln, sr, B, scale, cap, slopes, 1, ws, 0, None)
 
 
 def test_c_attention_refuses_on_the_host():
@@ -216,6 +216,8 @@ def test_c_attention_refuses_on_the_host():
     assert attn(Hq=3, Hkv=2) == attn(Hq=0) == attn(Hkv=0) == attn(t=-1) == attn(B=-1) == attn(d=132) == _lib.ERR_SHAPE
     assert attn(cap=-1.0) == attn(cap=math.inf) == attn(scale=math.nan) == attn(width=-1) == attn(size=12) == _lib.ERR_SHAPE
     assert attn(t=1 << 29, Hq=4) == attn(st={2: 64}) == attn(width=1 << 28) == _lib.ERR_SHAPE
+    assert attn(t=1, Hq=257) == attn(width=(1 << 22) + 1) == attn(scale=1e-15, slopes=P) == _lib.ERR_SHAPE
+    assert attn(t=1, Hq=256, Q=None) == attn(width=1 << 22, Q=None) == attn(scale=0.0, slopes=P, Q=None) == _lib.ERR_NULL
     assert attn(Q=None) == attn(Out=None) == attn(tb=None) == attn(ln=None) == attn(sr=None) == _lib.ERR_NULL
     assert attn(Q=ODD) == attn(ws=ODD) == attn(sr=ODD) == attn(st={3: 68}) == _lib.ERR_ALIGN
     assert attn(t=0, Q=None) == attn(B=0, Q=None) == _lib.OK
