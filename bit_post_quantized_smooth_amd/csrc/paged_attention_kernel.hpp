@@ -16,9 +16,10 @@
 // Two kinds of row tiles, by a sequence's own rows, in one launch, so that single
 // tokens and chunks of prompts run side by side:
 //   up to 32 rows (single tokens): the waves of a workgroup take blocks of 32 keys in
-//   turn. Each has its own part of LDS and fetches the next block into registers before
-//   it works on one (64 KB of codes in flight per compute unit, or 128 KB), with no
-//   barrier until the four add up their outputs at the end;
+//   turn. Each has its own part of LDS and fetches its next block into registers before
+//   it works on one (64 KB of codes in flight per compute unit, 128 KB of 16 bits; two
+//   blocks of codes ahead do not fit the registers), with no barrier until the four add
+//   up their outputs at the end;
 //   more rows: 128 per workgroup, 32 a wave, sharing tiles of 64 keys in two stages;
 //   16-bit tiles go straight into LDS, codes through registers, widened on the way.
 //
@@ -28,6 +29,17 @@
 // balance whatever the lengths are. Where a share's border falls into a tile the keys
 // are split there, each part writes fp32 outputs with their maxima and sums, and a
 // second kernel joins them in order. Tiles of little work are left whole.
+//
+// What bounds it. Single tokens: memory, and a tile's start (the lengths, a place on the
+// line, page numbers and the first keys are loads behind each other: 7 us) and end (2 us).
+// One token for each of 8 sequences of up to 8191, 32/8 heads of 128, e4m3: 25 us, of them
+// 15 at 7 TB/s (105 MB, part of them in the last-level cache), and 4.5 to join; 64 sequences of
+// 8191: 157 us, 5.2 TB/s; 1024 of 300, whose tiles are all start and end: 180 us, 2.7 TB/s.
+// Chunks: the softmax's vector work, 7 vector instructions per matrix instruction, beside
+// which the matrix cores are busy 37%: 4095 tokens at the end of 16383, 32/8 heads, e4m3, 1.08
+// ms with 17 us to join the parts, 890 TFLOP/s. Widening codes takes 4 to 9% of it (fp16: 1037 to
+// 1073 us with 16-bit pages beside 1118 to 1135). Its LDS writes meet in banks; in another order
+// they do not, and the kernel takes as long (1136 us beside 1137).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -435,10 +447,10 @@ struct ManyRows : PagedTile<T, DP, 4, CAP, SLOPES, CODED> {
       if (t > t0) get(t - 1, 1);
     }
     // From the last tile to the first: with slopes the largest scores come first, and the
-    // outputs are not rescaled for every tile (16 sequences, 3 chunks: 138 -> 117 us). The
-    // wave sees nothing from tile `off` on; all its rows see all keys of the tiles before
-    // `out`, but for pages that are missing: from the first of those on every tile is
-    // masked. A loop for each, as one with branches would copy the outputs.
+    // outputs are not rescaled for every tile (13 single tokens beside 3 chunks, slopes of 24
+    // heads: 138 -> 117 us). The wave sees nothing from tile `off` on; all its rows see all keys
+    // of the tiles before `out`, but for pages that are missing: from the first of those on every
+    // tile is masked. A loop for each, as one with branches would copy the outputs.
     const int off = max(t0, min(t1, (hi + KT - 1) / KT)), out = CAREFUL ? t0 : max(t0, min(off, hi_min / KT));
     auto begin = [&]() {
       const int s = (t1 - 1 - t) & 1;

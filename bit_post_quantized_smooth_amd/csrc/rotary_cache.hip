@@ -14,9 +14,16 @@
 // 448 s are clamped to it, infinities become the NaN code, so that they are not lost.
 //
 // Bound by memory: each element is read once and written once. 16 lanes (8 up to
-// 64 channels) hold a head, 8 channels each, and take several heads of one token
-// in turn, so that the angles' sines and cosines are computed once for them and
-// their loads are in flight together.
+// 64 channels) hold a head, 8 channels each. A workgroup takes one operand's heads, up to
+// four of a token per lane, so that the angles' sines and cosines are computed once for
+// them and their loads are in flight together. Sums over a head and the exchange of halves are
+// lane moves inside the vector unit; only a rotation of part of the head goes through LDS, and
+// one whose halves begin inside a lane's channels reads the partners from memory again.
+//
+// Measured: 4608 tokens of 24 + 24 heads of 128, fp16, norm and rotation: 24.7 us, 4.6 TB/s (a
+// copy of as many bytes 23.3); 8191 tokens, 32/8 heads into e4m3 pages: 42.5 us, 4.3 TB/s (35.8);
+// one token 3.6 us, and 5.9 with its call. Operands chosen per lane, with branches around each load:
+// 49 and 98 us. Reads of 8 sequences of up to 8191 out of e4m3 pages: 65 us, 4.8 TB/s (59.1).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
