@@ -211,6 +211,8 @@ int svdq_paged_write(const void* Q, const void* K, const void* V, void* Q_out, i
     return fail(SVDQ_ERR_ALIGN, fn, "heads must be 16-byte aligned, slots 4-byte");
   if (rows_overlap(strides + 6, T, Hq, D))
     return fail(SVDQ_ERR_SHAPE, fn, "the strides of Q_out make it overlap itself");
+  if (pages > 0 && k_pages == v_pages)
+    return fail(SVDQ_ERR_SHAPE, fn, "keys and values into the same pages");
   if (Q == Q_out && Hq > 0 && (strides[0] != strides[6] || strides[1] != strides[7]))
     return fail(SVDQ_ERR_SHAPE, fn, "in place with other strides");
   if (int s = device_ready(fn)) return s;

@@ -797,7 +797,8 @@ int svdq_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, int
  *   e4m3_rne(clamp(u * fp32(1 / scale), -448, 448)); NaN and infinities: the NaN code.
  * A token whose slot is not in the pool (-1, say) stores nothing; its queries are
  * written all the same. Slots in the pool must differ: where two tokens share one, any
- * mixture of the two is stored. strides: (token, head) of Q, K, V and Q_out. Hq = 0
+ * mixture of the two is stored. The pages of keys and of values share no bytes; two
+ * pools of one address are refused. strides: (token, head) of Q, K, V and Q_out. Hq = 0
  * writes keys and values alone. */
 int svdq_paged_write(const void* Q, const void* K, const void* V, void* Q_out, int dtype, int64_t T,
                      int64_t Hq, int64_t Hkv, int64_t D, const int64_t* strides,

@@ -226,3 +226,8 @@ def test_c_attention_refuses_on_the_host():
 def test_workspace_of_what_is_refused():
     assert sq.paged_attention_workspace_bytes(4, 1, 4000, 3, 2, 64) == 0
     assert sq.paged_attention_workspace_bytes(-1, 1, 4000, 2, 2, 64) == 0
+
+
+def test_c_write_refuses_one_memory_for_keys_and_values():
+    assert write(kp=P) == _lib.ERR_SHAPE                     # keys and values into the same bytes, in any order
+    assert write(kp=P, pages=0, t=0) == _lib.OK
