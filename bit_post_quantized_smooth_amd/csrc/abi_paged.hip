@@ -99,6 +99,9 @@ int check_rotation(const char* fn, const int32_t* positions, const double* freqs
   if (!std::isfinite(factor)) return fail(SVDQ_ERR_SHAPE, fn, "factor is not finite");
   if (pairs > 0 && (!positions || !freqs)) return fail(SVDQ_ERR_NULL, fn, "null pointer");
   if (!std::isfinite(eps)) return fail(SVDQ_ERR_SHAPE, fn, "eps is not finite");
+  // the reciprocal root takes a subnormal mean for 0: a head of zeros would become NaN
+  if (std::fpclassify(eps) == FP_SUBNORMAL)
+    return fail(SVDQ_ERR_SHAPE, fn, "eps is below fp32's normal numbers");
   if (eps < 0.f && (q_gain || k_gain)) return fail(SVDQ_ERR_SHAPE, fn, "a gain needs the norm");
   if (!aligned(positions, 4) || !aligned(freqs, 8) || !aligned(q_gain, 4) || !aligned(k_gain, 4))
     return fail(SVDQ_ERR_ALIGN, fn, "positions, freqs and gains need their element's alignment");

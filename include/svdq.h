@@ -777,8 +777,8 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
  */
 
 /* Device: norm and rotation of query and key heads in one pass, fp32, rounded once:
- *   u = x / sqrt(mean(x^2) + eps) * gain   over each head (eps < 0: without; a gain is
- *                                          D fp32 values or NULL);
+ *   u = x / sqrt(mean(x^2) + eps) * gain   over each head (eps < 0: without; else 0 or at
+ *                                          least 2^-126; a gain is D fp32 values or NULL);
  *   pair i of `pairs` turns by the angle positions[t] * freqs[i] radians (fp64):
  *     (a, b) <- factor * (a cos - b sin, a sin + b cos),
  *     channels (i, i + pairs), or (2i, 2i + 1) if interleaved; channels from

@@ -231,3 +231,10 @@ def test_workspace_of_what_is_refused():
 def test_c_write_refuses_one_memory_for_keys_and_values():
     assert write(kp=P) == _lib.ERR_SHAPE                     # keys and values into the same bytes, in any order
     assert write(kp=P, pages=0, t=0) == _lib.OK
+
+
+@pytest.mark.parametrize("eps", [1e-40, 1.1e-38])
+def test_c_eps_below_normal_numbers_refused(eps):
+    k = C.c_void_p(1 << 22)
+    out = C.c_void_p(1 << 24)
+    assert rot(K=k, Qo=out, Ko=C.c_void_p(1 << 26), eps=eps) == _lib.ERR_SHAPE
