@@ -293,6 +293,8 @@ class AttentionBlock:
             raise ValueError(f"X: shape {tuple(X.shape)}, expected (batch, tokens, {self.K})")
         if positions is not None and (self.turn is None or self.turn["freqs"] is None):
             raise ValueError("positions: the block has no rotation")
+        if positions is not None and not isinstance(positions, torch.Tensor):
+            raise TypeError(f"positions: expected a torch tensor, got {type(positions).__name__}")
         if residual is not None and residual.shape != X.shape:
             raise ValueError(f"residual: shape {tuple(residual.shape)}, X has {tuple(X.shape)}")
         if isinstance(cache, PagedKeyValueCache):
@@ -304,6 +306,8 @@ class AttentionBlock:
                 raise ValueError(f"X: {rows} rows, the step has {table.tokens} tokens (of up to "
                                  f"{table.step_tokens})")
             return self._run(X, residual, cache, causal, None, None, None)
+        if positions is not None and positions.shape != X.shape[:2]:
+            raise ValueError(f"positions: shape {tuple(positions.shape)}, expected {tuple(X.shape[:2])}")
         held = None if cache is None else cache.length
         try:
             return self._run(X, residual, cache, causal, prefix, key_ranges, positions)
@@ -338,8 +342,6 @@ class AttentionBlock:
                     positions = None
                 elif positions is None:
                     positions = self._positions(B, L, 0 if cache is None else cache.length)
-                elif positions.shape != (B, L):
-                    raise ValueError(f"positions: shape {tuple(positions.shape)}, expected {(B, L)}")
                 x = t.view(M, Hq + 2 * Hkv, D)
                 q, k = x[:, :Hq], x[:, Hq:Hq + Hkv]
                 paged.norm_rotary(q, k, q, k, positions=None if positions is None else positions.reshape(M),

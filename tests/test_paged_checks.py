@@ -238,3 +238,13 @@ def test_c_eps_below_normal_numbers_refused(eps):
     k = C.c_void_p(1 << 22)
     out = C.c_void_p(1 << 24)
     assert rot(K=k, Qo=out, Ko=C.c_void_p(1 << 26), eps=eps) == _lib.ERR_SHAPE
+
+
+def test_block_positions_must_be_a_tensor():
+    w = np.zeros((64, 3 * 64), np.float32)
+    block = sq.AttentionBlock(np.ones(64, np.float32), sq.prepare_weights_fp8(w), sq.prepare_weights_fp8(w[:, :64]), 1, 1, 64,
+                              device="cpu", rotary=sq.rotary_frequencies(64))
+    with pytest.raises(TypeError, match="positions"):
+        block(z(1, 2, 64), positions=[0, 1])
+    with pytest.raises(ValueError, match="positions"):
+        block(z(1, 2, 64), positions=z(1, 3, dtype=i32))
