@@ -37,9 +37,9 @@
 // 8191: 157 us, 5.2 TB/s; 1024 of 300, whose tiles are all start and end: 180 us, 2.7 TB/s.
 // Chunks: the softmax's vector work, 7 vector instructions per matrix instruction, beside
 // which the matrix cores are busy 37%: 4095 tokens at the end of 16383, 32/8 heads, e4m3, 1.08
-// ms with 17 us to join the parts, 890 TFLOP/s. Widening codes takes 4 to 9% of it (fp16: 1037 to
-// 1073 us with 16-bit pages beside 1118 to 1135). Its LDS writes meet in banks; in another order
-// they do not, and the kernel takes as long (1136 us beside 1137).
+// to 1.11 ms with 17 us to join the parts, 870 to 890 TFLOP/s. Widening codes takes 4 to 9% of
+// it (fp16: 1037 to 1073 us with 16-bit pages beside 1118 to 1135). Its LDS writes meet in
+// banks; in another order they do not, and the kernel takes as long (1136 us beside 1137).
 #pragma once
 
 #include <hip/hip_runtime.h>

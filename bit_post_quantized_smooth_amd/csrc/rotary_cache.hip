@@ -22,7 +22,7 @@
 //
 // Measured: 4608 tokens of 24 + 24 heads of 128, fp16, norm and rotation: 24.7 us, 4.6 TB/s (a
 // copy of as many bytes 23.3); 8191 tokens, 32/8 heads into e4m3 pages: 42.5 us, 4.3 TB/s (35.8);
-// one token 3.6 us, and 5.9 with its call. Operands chosen per lane, with branches around each load:
+// one token 3.6 us, and 5.9 to 6.4 with its call. Operands chosen per lane, with branches around each load:
 // 49 and 98 us. Reads of 8 sequences of up to 8191 out of e4m3 pages: 65 us, 4.8 TB/s (59.1).
 #include <hip/hip_runtime.h>
 
