@@ -196,15 +196,15 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs g) {
     float u[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) u[e] = static_cast<float>(raw[i][e]);
-    float rstd = 1.f;
+    float root = 1.f, unit = 1.f;
     if (norm) {
       float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sum = __builtin_fmaf(u[e], u[e], sum);
       float mean = __builtin_fmaf(row_sum<LPR>(inside ? sum : 0.f), g.inv_D, g.eps);
-      float unit = 1.f;
       // squares beyond fp32 (bf16 values above 2^63) or below it (with an eps as small):
-      // of values in units of the row's largest
+      // of values in units of the row's largest. The values take the unit before the root:
+      // the two multiplied can leave fp32 (a row below 2^-128).
       const bool far = !(mean >= 0x1p-100f && mean < __builtin_inff());
       if (__builtin_amdgcn_ballot_w64(far) != 0) {
         float top = 0.f;
@@ -215,14 +215,17 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs g) {
           unit = __builtin_ldexpf(1.f, min(max(-__builtin_amdgcn_frexp_expf(top), -126), g.most_unit));
           sum = 0.f;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) sum = __builtin_fmaf(u[e] * unit, u[e] * unit, sum);
+          for (int e = 0; e < VEC; ++e) {
+            u[e] = u[e] * unit;
+            sum = __builtin_fmaf(u[e], u[e], sum);
+          }
         }
         sum = row_sum<LPR>(inside ? sum : 0.f);
         if (unit != 1.f) mean = __builtin_fmaf(sum, g.inv_D, g.eps * unit * unit);
       }
-      rstd = __builtin_amdgcn_rsqf(mean) * unit;
+      root = __builtin_amdgcn_rsqf(mean);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) u[e] = u[e] * rstd * gains[e];
+      for (int e = 0; e < VEC; ++e) u[e] = u[e] * root * gains[e];
     }
     if (turn) {
       float p[VEC];
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs g) {
         for (int e = 0; e < VEC; ++e) {
           const int ch = c0 + e, other = ch >= R ? 0 : ch < g.pairs ? ch + g.pairs : ch - g.pairs;
           p[e] = static_cast<float>(x[other]);
-          if (norm) p[e] = p[e] * rstd * (gain != nullptr ? gain[other] : 1.f);
+          if (norm) p[e] = p[e] * unit * root * (gain != nullptr ? gain[other] : 1.f);
         }
       }
 #pragma unroll
