@@ -1,13 +1,14 @@
 // The rotation of a head's channels by a position (gfx950).
 //
 // Channel pairs (a, b) turn by position * freq radians. The angle is formed and
-// reduced in fp64, in whole turns: position * (freq / 2 pi) is good to 2^-52 of
-// itself, so at position 2^20 the fraction of a turn is good to 2^-30, where an
-// fp32 angle would be off by 2^-4 radians. What is left, at most an eighth of a
+// reduced in fp64, in whole turns: position * (freq / 2 pi) is good to 3 * 2^-53 of
+// itself, so at an angle of 2^20 radians it is good to 2^-31 of one, where an fp32 angle
+// would be off by 2^-4. At 2^28 radians that is 2^-23.4, less than fp32's roundings
+// behind it; at 2^31 it is 2^-20.4 and exceeds them. What is left, at most an eighth of a
 // turn, goes through the Taylor polynomials of sine (to x^9) and cosine (to x^8),
-// whose next terms are below 2e-9 and 3e-8, less than an fp32 rounding. Four fp64
-// instructions and 20 fp32 ones per pair and token, shared by the token's heads:
-// a table of cosines would cost a load of as many bytes as a head.
+// whose next terms are below 2e-9 and 3e-8, less than an fp32 rounding. Nine fp64
+// instructions, three conversions and 20 fp32 ones per pair and token, shared by the
+// token's heads: a table of cosines would cost a load of as many bytes as a head.
 #pragma once
 
 #include "block_common.hpp"

@@ -783,7 +783,8 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
  *     (a, b) <- factor * (a cos - b sin, a sin + b cos),
  *     channels (i, i + pairs), or (2i, 2i + 1) if interleaved; channels from
  *     2 * pairs on stay as they are. pairs = 0: no rotation.
- * A cosine is good to 2^-22 for positions * freqs up to 2^31. strides: 8 element
+ * A cosine is good to 2^-22 for |positions * freqs| up to 2^28, to 2^-20 up to 2^31 (the
+ * angle is formed in fp64, whose step has grown to that). strides: 8 element
  * strides, (token, head) of Q, K, Q_out and K_out. Hq or Hkv may be 0. Q_out may be Q,
  * and K_out K, with the same strides; outputs may not overlap the inputs otherwise. */
 int svdq_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, int dtype, int64_t T,
