@@ -170,7 +170,7 @@ class PageTable:
 class PagedKeyValueCache:
     """One layer's keys and values in the pages of a PageTable, of the layer's 16-bit type or
     (``dtype`` torch.float8_e4m3fn) as e4m3 codes of one scale per head: ``k_scales``,
-    ``v_scales``, fp32, kv_heads values above 0, by default 1. Values beyond 448 scales are
+    ``v_scales``, fp32, kv_heads values in 2^-64 .. 2^64, by default 1. Values beyond 448 scales are
     clamped, those below 2^-9 of one vanish."""
 
     def __init__(self, table: PageTable, kv_heads: int, head_dim: int, dtype, k_scales=None, v_scales=None):
@@ -187,8 +187,9 @@ class PagedKeyValueCache:
             x = np.asarray(x, np.float32)
             if dtype is not torch.float8_e4m3fn:
                 raise ValueError(f"{name}: 16-bit pages have none")
-            if x.shape != (kv_heads,) or not np.all((x > 0) & np.isfinite(x)):
-                raise ValueError(f"{name}: expected {kv_heads} finite values above 0")
+            # beyond, their reciprocals or their products with the scores' scale leave fp32
+            if x.shape != (kv_heads,) or not np.all((x >= 2.0 ** -64) & (x <= 2.0 ** 64)):
+                raise ValueError(f"{name}: expected {kv_heads} values in 2^-64 .. 2^64")
         put = lambda x: None if x is None else torch.from_numpy(api._c(x, np.float32)).to(table.device)  # noqa: E731
         self.k_scales, self.v_scales = put(k_scales), put(v_scales)
 

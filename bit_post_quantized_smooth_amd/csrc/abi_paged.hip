@@ -340,9 +340,13 @@ int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t
   if (int s = check_paged_attention_sizes(fn, T, B, capacity, Hq, Hkv, D)) return s;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f)
     return fail(SVDQ_ERR_SHAPE, fn, "scale and softcap must be finite, softcap not negative");
-  // slopes are kept in units of the scores, which may not leave fp32
-  if (slopes && scale != 0.f && std::fabs(scale) < 0x1p-40f)
-    return fail(SVDQ_ERR_SHAPE, fn, "a scale below 2^-40 with slopes");
+  // Slopes are kept in units of the scores, and key scales (2^-64 .. 2^64, on the device)
+  // multiply the scale: neither may leave fp32. A product of 0 would make a masked score
+  // -inf * 0, an infinite one a score of 0.
+  if ((slopes || k_scales) && scale != 0.f && std::fabs(scale) < 0x1p-40f)
+    return fail(SVDQ_ERR_SHAPE, fn, "a scale below 2^-40 with slopes or key scales");
+  if (k_scales && std::fabs(scale) > 0x1p60f)
+    return fail(SVDQ_ERR_SHAPE, fn, "a scale above 2^60 with key scales");
   if (T == 0 || B == 0) return SVDQ_OK;
   if (rows_overlap(strides + 2, T, Hq, D))
     return fail(SVDQ_ERR_SHAPE, fn, "the strides of Out make it overlap itself");

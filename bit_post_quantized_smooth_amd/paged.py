@@ -283,8 +283,8 @@ def norm_rotary_write(Q, K, V, Q_out, slots, k_pages, v_pages, k_scales=None, v_
     """svdq_paged_write: norm_rotary with the keys, and the values V (T x Hkv x D) as they are,
     stored into the pages at ``slots`` (int32, T: page * page size + place in the page; a token
     whose slot is outside the pool, such as -1, is stored nowhere). Slots in the pool must
-    differ. k_scales, v_scales (fp32, Hkv): the scales of e4m3 pages; values beyond 448 scales
-    are clamped."""
+    differ. k_scales, v_scales (fp32, Hkv, 2^-64 .. 2^64): the scales of e4m3 pages; values beyond
+    448 scales are clamped."""
     try:
         T, Hkv, D = shape = K.shape
         dtype = K.dtype
@@ -399,7 +399,8 @@ def paged_attention(Q, k_pages, v_pages, tables, lengths, starts, Out, k_scales=
     are the last of its lengths[b] (int32, B) tokens in the pages tables[b] (int32, B x width),
     their own keys and values written before.
 
-    scale: of the scores, D**-0.5 by default; softcap, slopes: as in attention(); causal: a
+    scale: of the scores, D**-0.5 by default, its size with k_scales 0 or 2^-40 .. 2^60 (with
+    slopes 0 or from 2^-40 on); softcap, slopes: as in attention(); causal: a
     token sees the keys up to its own position, else all of its sequence. A row that sees no
     key is 0, rows of no sequence are left as they were. With a workspace of
     paged_attention_workspace_bytes(T, B, width * page size, Hq, Hkv, D) work is split along
