@@ -234,6 +234,9 @@ class AttentionBlock:
                            ("head_gains", q_gain, head_dim), ("head_gains", k_gain, head_dim)):
             if x is not None and math.prod(np.shape(x)) != n:
                 raise ValueError(f"{name}: shape {tuple(np.shape(x))}, expected {n} values")
+        # as norm_rotary takes it, in fp32
+        if head_gains is not None and not (eps == 0 or (2.0 ** -126 <= np.float32(eps) < math.inf)):
+            raise ValueError(f"eps: {eps}, norms of heads take 0 or a finite value from 2^-126 on")
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.eps, self.softcap = float(eps), float(softcap)
         dev = self.device = torch.device(device)
@@ -306,9 +309,17 @@ class AttentionBlock:
             if not table.tokens <= rows <= table.step_tokens:
                 raise ValueError(f"X: {rows} rows, the step has {table.tokens} tokens (of up to "
                                  f"{table.step_tokens})")
+            held = cache.k
+            if held.dtype not in (X.dtype, torch.float8_e4m3fn) or held.device != X.device:
+                raise ValueError(f"cache: {held.dtype} on {held.device}, X has {X.dtype} on {X.device}")
+            if (held.shape[1], held.shape[3]) != (self.kv_heads, self.head_dim):
+                raise ValueError(f"cache: {held.shape[1]} heads of {held.shape[3]}, the block has "
+                                 f"{self.kv_heads} of {self.head_dim}")
             return self._run(X, residual, cache, causal, None, None, None)
         if positions is not None and positions.shape != X.shape[:2]:
             raise ValueError(f"positions: shape {tuple(positions.shape)}, expected {tuple(X.shape[:2])}")
+        if positions is not None and (positions.dtype is not torch.int32 or positions.device != X.device):
+            raise ValueError(f"positions: {positions.dtype} on {positions.device}, expected int32 on {X.device}")
         held = None if cache is None else cache.length
         try:
             return self._run(X, residual, cache, causal, prefix, key_ranges, positions)
