@@ -277,7 +277,10 @@ struct AttentionCore {
     return 1.f;
   }
 
-  // x -> P in 16 bits (the operands of 16 keys each)
+  // x -> P in 16 bits (the operands of 16 keys each). The rounding is a choice: weights
+  // in fp32 would need two 16-bit operands each, twice the second product's matrix
+  // instructions. A bf16 output is off by 0.0022 to 0.0024 of its norm with it, 0.0017 by its own
+  // rounding alone; fp16 0.00026 to 0.0003 and 0.00021 (prompts and single tokens).
   __device__ __forceinline__ void exponentials(const v16f& x, float scale, vec (&p)[2]) {
     const float sub = base();
 #pragma unroll

@@ -739,8 +739,9 @@ size_t svdq_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t
  *   key_ranges (NULL, or [begin, end) int32 pairs per batch entry and query;
  *   values outside 0 .. Lk are cut) and, if causal, j <= pos_i or j < prefix[b]
  *   (prefix: NULL or one int32 per batch entry; only with causal).
- * A row that sees no key is 0; a key that a row does not see does not reach its
- * output even where its K or V hold infinities or NaN.
+ * A row that sees no key is 0; a key that a row does not see is no part of its
+ * output even where its K or V hold infinities or NaN (the last bits of rows beside
+ * such a V may differ: they are computed again in another order).
  * Scores, maxima, sums and outputs are fp32; a softmax weight is rounded once to the
  * type of V, in f16 to a multiple of at most 2^-34 of the row's largest weight.
  * dtype (f16, bf16) is that of Q, K, V and Out. Query head h reads key head
@@ -834,9 +835,12 @@ size_t svdq_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t capaci
  *   x[i][j] = scale * k_scale * q_i . k_j; softcap and slopes as in svdq_attention;
  *   out_i = v_scale * sum_j softmax_j(x[i][j]) v_j over the keys j < lengths[b] in
  *   pages of the pool with, if causal, j <= position of i.
- * Keys and values are the pages' values or codes. A row that sees no key is 0; a key
- * that a row does not see does not reach its output whatever its page holds. Rows of
- * no sequence are left as they were. strides: (token, head) of Q and Out, which may not
+ * Keys and values are the pages' values or codes. A row that sees no key is 0. A key
+ * that a row does not see is no part of its output whatever its page holds; but where
+ * that is not finite, the rows that share its tile are computed again in another order,
+ * with roundings of the same size whose last bits differ. Scores, maxima, sums and
+ * outputs are fp32; a softmax weight is rounded once to the type of Q, as in
+ * svdq_attention. Rows of no sequence are left as they were. strides: (token, head) of Q and Out, which may not
  * overlap. T * Hq: up to 2^30; width * page_size: up to 2^26; Hq / Hkv: up to 256; |scale|:
  * with slopes or k_scales 0 or at least 2^-40, with k_scales up to 2^60; slopes: up to
  * 2^20. ws: NULL or a 16-byte aligned workspace; with at least
