@@ -96,6 +96,12 @@ class PageTable:
         self.width = -(-capacity // page_size)
         self.pages = batch * self.width if pages is None else pages
         self.step_tokens = batch * capacity if step_tokens is None else step_tokens
+        if self.width * page_size > 2 ** 26:
+            raise ValueError(f"capacity: {capacity}, attention takes up to 2^26 keys of a sequence")
+        if self.pages < 0 or self.pages * page_size > 2 ** 31:
+            raise ValueError(f"pages: {self.pages} of {page_size} tokens, expected up to 2^31 tokens")
+        if self.step_tokens < 0:
+            raise ValueError(f"step_tokens: {self.step_tokens}")
         self.tokens = 0                           # of the step that was begun last
         self.device = torch.device(device)
         sizes = [batch * self.width, batch, batch + 1, self.step_tokens, self.step_tokens]
@@ -132,6 +138,8 @@ class PageTable:
         n = np.broadcast_to(n, (self.batch,)).astype(np.int64) if n.ndim == 0 else n.astype(np.int64)
         if n.shape != (self.batch,) or np.any(n < 0):
             raise ValueError(f"counts: expected {self.batch} numbers >= 0")
+        if np.any(n > self.capacity):             # before sums that could wrap
+            raise ValueError(f"sequences of up to {self.capacity} tokens: {int(n.max())} more needed")
         total, after = int(n.sum()), self._lengths + n
         if total > self.step_tokens:
             raise ValueError(f"{total} tokens in a step of up to {self.step_tokens}")
@@ -143,6 +151,11 @@ class PageTable:
             raise ValueError(f"{int((need - have).sum())} pages needed, {len(self._free)} are free")
         if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
             raise RuntimeError("begin: while a graph is captured; call it before each replay")
+        # tables, lengths, starts and slots lie one behind the other: one copy, with -1 for
+        # the slots that the step before used and this one does not
+        used = max(total, self._written)
+        fixed = self._tables.size + 2 * self.batch + 1
+        host = torch.empty(fixed + used + total, dtype=torch.int32, pin_memory=self.device.type == "cuda")
         for b in np.nonzero(need > have)[0]:
             for i in range(have[b], need[b]):
                 self._tables[b, i] = self._free.pop()
@@ -151,11 +164,6 @@ class PageTable:
         position = np.arange(total) - starts[sequence] + self._lengths[sequence]
         self._lengths = after
         self.tokens = total
-        # tables, lengths, starts and slots lie one behind the other: one copy, with -1 for
-        # the slots that the step before used and this one does not
-        used = max(total, self._written)
-        fixed = self._tables.size + 2 * self.batch + 1
-        host = torch.empty(fixed + used + total, dtype=torch.int32, pin_memory=self.device.type == "cuda")
         h = host.numpy()
         h[:self._tables.size] = self._tables.ravel()
         h[self._tables.size:fixed] = np.concatenate((after, starts))
