@@ -164,6 +164,8 @@ int svdq_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, int
   if ((Q == Q_out && Hq > 0 && (strides[0] != strides[4] || strides[1] != strides[5])) ||
       (K == K_out && Hkv > 0 && (strides[2] != strides[6] || strides[3] != strides[7])))
     return fail(SVDQ_ERR_SHAPE, fn, "in place with other strides");
+  if (Hq > 0 && Hkv > 0 && Q_out == K_out)
+    return fail(SVDQ_ERR_SHAPE, fn, "queries and keys into the same output");
   if (int s = device_ready(fn)) return s;
   HeadsArgs g{};
   g.q = Q;
@@ -275,6 +277,7 @@ int svdq_paged_read(const void* k_pages, const void* v_pages, int cache_dtype, i
     if (overlaps(dims, D))
       return fail(SVDQ_ERR_SHAPE, fn, "the strides of an output make it overlap itself");
   }
+  if (K_out == V_out) return fail(SVDQ_ERR_SHAPE, fn, "keys and values into the same output");
   if (int s = device_ready(fn)) return s;
   g.tables = tables;
   g.lengths = lengths;

@@ -220,7 +220,7 @@ def norm_rotary(Q, K, Q_out, K_out, positions=None, freqs=None, factor: float = 
                 stream=None):
     """svdq_norm_rotary: query heads Q (T x Hq x D) and key heads K (T x Hkv x D, or None
     with K_out), fp16 or bf16, strided views with contiguous channels, into Q_out and K_out
-    (which may be Q and K).
+    (which may be Q and K, but not one memory).
 
     eps: the RMS norm of each head, times q_gain and k_gain (fp32, D); None: no norm.
     positions (int32, T) and freqs (fp64, radians per position of each pair:
@@ -349,8 +349,8 @@ def paged_read(k_pages, v_pages, tables, lengths, K_out, V_out, k_scales=None, v
                stream=None):
     """svdq_paged_read: the first lengths[b] (int32, B) tokens of each sequence out of the pages
     tables[b] (int32, B x width) into K_out and V_out (B x L x Hkv x D, fp16 or bf16; of 16-bit
-    pages the same type), codes times their scales. Rows behind a sequence's length are left as
-    they were."""
+    pages the same type; not one memory), codes times their scales. Rows behind a sequence's
+    length are left as they were."""
     try:
         B, L, Hkv, D = shape = K_out.shape
         dtype = K_out.dtype

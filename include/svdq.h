@@ -788,7 +788,8 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
  * A cosine is good to 2^-22 for |positions * freqs| up to 2^28, to 2^-20 up to 2^31 (the
  * angle is formed in fp64, whose step has grown to that). strides: 8 element
  * strides, (token, head) of Q, K, Q_out and K_out. Hq or Hkv may be 0. Q_out may be Q,
- * and K_out K, with the same strides; outputs may not overlap the inputs otherwise. */
+ * and K_out K, with the same strides; outputs may not overlap the inputs otherwise, nor
+ * each other (one address for both is refused). */
 int svdq_norm_rotary(const void* Q, const void* K, void* Q_out, void* K_out, int dtype, int64_t T,
                      int64_t Hq, int64_t Hkv, int64_t D, const int64_t* strides,
                      const int32_t* positions, const double* freqs, int64_t pairs, float factor,
@@ -815,7 +816,8 @@ int svdq_paged_write(const void* Q, const void* K, const void* V, void* Q_out, i
 /* Device: sequences back from their pages, K_out and V_out (B x L x Hkv x D) in f16 or
  * bf16 (16-bit pages: of the same type): token j < lengths[b] of sequence b, code *
  * scale rounded once. Rows from lengths[b] on, and of pages outside the pool, are left
- * as they were. strides: (batch, token, head) of K_out and V_out. */
+ * as they were. strides: (batch, token, head) of K_out and V_out, which may not overlap
+ * (one address for both is refused). */
 int svdq_paged_read(const void* k_pages, const void* v_pages, int cache_dtype, int64_t pages,
                     int64_t page_size, int64_t k_page_stride, int64_t v_page_stride,
                     const float* k_scales, const float* v_scales, const int32_t* tables,
