@@ -10,6 +10,7 @@
 #include <utility>
 
 #include "../../include/svdq.h"
+#include "abi_checks.hpp"
 #include "attention.hpp"
 #include "block_launch.hpp"
 #include "host_internal.hpp"
@@ -20,35 +21,8 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxK = int64_t{1} << 22;      // 256 rows of codes stay below 2^31 bytes
-constexpr int64_t kMaxStride = int64_t{1} << 40;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-int fail(int status, const char* fn, const char* what) {
-  set_error("%s: %s", fn, what);
-  return status;
-}
-
-int device_ready(const char* fn) {
-  int dev = -1;
-  const hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess || dev < 0) {
-    (void)hipGetLastError();
-    set_error("%s: no usable GPU: %s", fn, hipGetErrorString(e));
-    return SVDQ_ERR_NO_DEVICE;
-  }
-  return SVDQ_OK;
-}
-
-int check_hip(hipError_t e, const char* fn) {
-  if (e != hipSuccess) {
-    set_error("%s launch: %s", fn, hipGetErrorString(e));
-    return SVDQ_ERR_HIP;
-  }
-  return SVDQ_OK;
-}
 
 bool known(int dtype) { return dtype == SVDQ_F16 || dtype == SVDQ_F32 || dtype == SVDQ_BF16; }
 uintptr_t esize(int dtype) { return dtype == SVDQ_F32 ? 4 : 2; }

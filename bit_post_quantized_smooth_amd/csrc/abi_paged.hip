@@ -11,6 +11,7 @@
 #include <utility>
 
 #include "../../include/svdq.h"
+#include "abi_checks.hpp"
 #include "attention.hpp"
 #include "block_launch.hpp"
 #include "host_internal.hpp"
@@ -21,35 +22,8 @@ using namespace svdq;
 
 namespace {
 
-constexpr int64_t kMaxStride = int64_t{1} << 40;
 constexpr int64_t kMaxTokens = int64_t{1} << 30;
 constexpr int64_t kMaxHeads = 65536;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-int fail(int status, const char* fn, const char* what) {
-  set_error("%s: %s", fn, what);
-  return status;
-}
-
-int device_ready(const char* fn) {
-  int dev = -1;
-  const hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess || dev < 0) {
-    (void)hipGetLastError();
-    set_error("%s: no usable GPU: %s", fn, hipGetErrorString(e));
-    return SVDQ_ERR_NO_DEVICE;
-  }
-  return SVDQ_OK;
-}
-
-int check_hip(hipError_t e, const char* fn) {
-  if (e != hipSuccess) {
-    set_error("%s launch: %s", fn, hipGetErrorString(e));
-    return SVDQ_ERR_HIP;
-  }
-  return SVDQ_OK;
-}
 
 int check_heads(const char* fn, int dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
   if (dtype != SVDQ_F16 && dtype != SVDQ_BF16)
