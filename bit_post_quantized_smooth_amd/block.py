@@ -179,7 +179,7 @@ class PagedKeyValueCache:
     """One layer's keys and values in the pages of a PageTable, of the layer's 16-bit type or
     (``dtype`` torch.float8_e4m3fn) as e4m3 codes of one scale per head: ``k_scales``,
     ``v_scales``, fp32, kv_heads values in 2^-64 .. 2^64, by default 1. Values beyond 448 scales are
-    clamped, those below 2^-9 of one vanish."""
+    clamped, those up to 2^-10 of one vanish."""
 
     def __init__(self, table: PageTable, kv_heads: int, head_dim: int, dtype, k_scales=None, v_scales=None):
         torch = api._torch()
@@ -217,7 +217,8 @@ class AttentionBlock:
     ``begin`` was last called for, sequence after sequence whatever batch and tokens X
     has, and the rows of Y behind them are not specified. Buffers are kept between calls and grown when more tokens arrive, so
     one block serves one stream at a time (the smaller ones stay, for graphs captured
-    with them), and Y and h are new tensors."""
+    with them), and Y and h are new tensors. Over a paged cache the attention's parts
+    take up to 68 MB of them in every block (heads of 128 channels)."""
 
     def __init__(self, gain, qkv, out, heads: int, kv_heads: int, head_dim: int,
                  qkv_bias=None, out_bias=None, eps: float = 1e-6, softcap: float = 0.0,

@@ -33,12 +33,16 @@
 // What bounds it. Single tokens: memory, and a tile's start (the lengths, a place on the
 // line, page numbers and the first keys are loads behind each other: 7 us) and end (2 us).
 // One token for each of 8 sequences of up to 8191, 32/8 heads of 128, e4m3: 25 us, of them
-// 15 at 7 TB/s (105 MB, part of them in the last-level cache), and 4.5 to join; 64 sequences of
-// 8191: 157 us, 5.2 TB/s; 1024 of 300, whose tiles are all start and end: 180 us, 2.7 TB/s.
-// Chunks: the softmax's vector work, 7 vector instructions per matrix instruction, beside
-// which the matrix cores are busy 37%: 4095 tokens at the end of 16383, 32/8 heads, e4m3, 1.08
-// to 1.11 ms with 17 us to join the parts, 870 to 890 TFLOP/s. Widening codes takes 4 to 9% of
-// it (fp16: 1037 to 1073 us with 16-bit pages beside 1118 to 1135). Its LDS writes meet in
+// 15 at 7 TB/s (105 MB, part of them in the last-level cache), and 4.5 to join; 16-bit pages 54
+// us with the join. 64 sequences of 8191: 194 us, 5.5 TB/s (16 bits 373, 5.8); 1024 of 300,
+// whose tiles are all start and end: 199 us, 3.25 TB/s (268, 4.75). The join is launched where
+// the table could hold a sequence long enough to cut, whatever the lengths are: one token over
+// 333 keys takes 9.4 us with a table of 336 places, 12.0 with one of 8192.
+// Chunks: neither unit alone; the vector unit is busy 41% of the time (the softmax, with 7
+// vector instructions per matrix instruction, and the issue of these) and the matrix cores
+// 36%, for the most part one after the other. 4095 tokens at the end of 16383, 32/8 heads, e4m3,
+// 1.08 to 1.12 ms with 17 us to join the parts, 860 to 890 TFLOP/s. Widening codes takes 1 to 4% of
+// it (16-bit pages: fp16 1101 us beside 1113, bf16 1041 beside 1083). Its LDS writes meet in
 // banks; in another order they do not, and the kernel takes as long (1136 us beside 1137).
 #pragma once
 

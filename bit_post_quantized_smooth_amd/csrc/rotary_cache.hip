@@ -5,7 +5,10 @@
 //     (a, b) <- factor * (a cos - b sin, a sin + b cos)
 //   queries, and keys without pages: rounded to 16 bits;
 //   keys and values with pages: rounded to 16 bits, or to codes
-//     e4m3_rne(clamp(u * fp32(1 / s), -448, 448)) with the head's scale s.
+//     e4m3_rne(clamp(u * fp32(1 / s), -448, 448)) with the head's scale s (two roundings of
+//     2^-24 where a division has one, so that a value as near a midpoint of two codes may
+//     take the other, for one instruction an element instead of ten; 1 / s is in fp32 for
+//     scales in 2^-64 .. 2^64).
 //
 // Sums, norms and rotations are fp32 and a value is rounded once. A code keeps a
 // relative precision of 2^-4 over 2^15 of range, so one scale per head, chosen
@@ -20,10 +23,10 @@
 // lane moves inside the vector unit; only a rotation of part of the head goes through LDS, and
 // one whose halves begin inside a lane's channels reads the partners from memory again.
 //
-// Measured: 4608 tokens of 24 + 24 heads of 128, fp16, norm and rotation: 24.7 us, 4.6 TB/s (a
-// copy of as many bytes 23.3); 8191 tokens, 32/8 heads into e4m3 pages: 42.5 us, 4.3 TB/s (35.8);
-// one token 3.6 us, and 5.9 to 6.4 with its call. Operands chosen per lane, with branches around each load:
-// 49 and 98 us. Reads of 8 sequences of up to 8191 out of e4m3 pages: 65 us, 4.8 TB/s (59.1).
+// Measured: 4608 tokens of 24 + 24 heads of 128, fp16, norm and rotation: 24.5 to 25 us, 4.6 TB/s (a
+// copy of as many bytes 23.3); 8191 tokens, 32/8 heads into e4m3 pages: 42.8 us, 4.3 TB/s (35.8);
+// one token 3.4 us, and 5.9 to 6.4 with its call. Operands chosen per lane, with branches around each load:
+// 49 and 98 us. Reads of 8 sequences of up to 8191 out of e4m3 pages: 65.7 us, 4.8 TB/s (59.1).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
