@@ -766,8 +766,8 @@ int svdq_attention(const void* Q, const void* K, const void* V, void* Out, int d
  * x page_size tokens x D channels, contiguous, of the tokens' type (f16, bf16) or as
  * e4m3 codes (cache_dtype SVDQ_E4M3) of one fp32 scale per head, 2^-64 to 2^64, so that
  * reciprocals and products with the scores' scale stay in fp32 (k_scales, v_scales: Hkv
- * values on the device, where nothing checks them; NULL: 1). A token's slot is page * page_size + its
- * place in the page. A sequence's token j lies in page tables[b][j / page_size]
+ * values on the device, where nothing checks them; NULL: 1). A token's slot is
+ * page * page_size + its place in the page. A sequence's token j lies in page tables[b][j / page_size]
  * (tables: B x width int32). Slots, tables, lengths and starts lie on the device, so
  * that one captured graph serves growing sequences; a slot or page outside the pool is
  * no place at all: nothing is stored there, read from there or seen there.
@@ -842,12 +842,12 @@ size_t svdq_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t capaci
  * that is not finite, the rows that share its tile are computed again in another order,
  * with roundings of the same size whose last bits differ. Scores, maxima, sums and
  * outputs are fp32; a softmax weight is rounded once to the type of Q, as in
- * svdq_attention. Rows of no sequence are left as they were. strides: (token, head) of Q and Out, which may not
- * overlap. T * Hq: up to 2^30; width * page_size: up to 2^26; Hq / Hkv: up to 256; |scale|:
- * with slopes or k_scales 0 or at least 2^-40, with k_scales up to 2^60; slopes: up to
- * 2^20. ws: NULL or a 16-byte aligned workspace; with at least
- * svdq_paged_attention_workspace_bytes bytes work is split along the keys. Two calls
- * that may run at once need a workspace each. */
+ * svdq_attention. Rows of no sequence are left as they were. strides: (token, head) of
+ * Q and Out, which may not overlap. T * Hq: up to 2^30; width * page_size: up to 2^26;
+ * Hq / Hkv: up to 256; |scale|: with slopes or k_scales 0 or at least 2^-40, with
+ * k_scales up to 2^60; slopes: up to 2^20. ws: NULL or a 16-byte aligned workspace; with
+ * at least svdq_paged_attention_workspace_bytes bytes work is split along the keys. Two
+ * calls that may run at once need a workspace each. */
 int svdq_paged_attention(const void* Q, void* Out, int dtype, int64_t T, int64_t Hq, int64_t Hkv,
                          int64_t D, const int64_t* strides, const void* k_pages,
                          const void* v_pages, int cache_dtype, int64_t pages, int64_t page_size,
